@@ -111,7 +111,7 @@ def _quantise_rows(x):
     """Codes and scales of the rows of x, fp32."""
     a = _group_amax(x)
     a = torch.where(a == 0, a, a.clamp(min=TINY))
-    r = torch.where(a == 0, a, E4M3_MAX / a)
+    r = torch.where(a == 0, a, torch.full_like(a, E4M3_MAX) / a)  # number / tensor would round twice
     return (x * _spread(r, x.shape[1])).to(torch.float8_e4m3fn), a / E4M3_MAX
 
 
@@ -250,7 +250,7 @@ def exact(case, seed):
     else:  # the codes are rounded by definition: in 32 bits, as it says
         a = torch.stack([c.abs().max(1).values for c in st["x"].float().split(GROUP, dim=1)], 1)
         a = torch.where(a > 0, a.clamp(min=TINY), a)
-        r = torch.where(a > 0, E4M3_MAX / a, a)
+        r = torch.where(a > 0, torch.full_like(a, E4M3_MAX) / a, a)
         group = torch.arange(case["K"], device="cuda") // GROUP
         codes, s = (st["x"].float() * r[:, group]).to(torch.float8_e4m3fn).double(), a.double() / E4M3_MAX
     y = torch.zeros(case["M"], case["N"], dtype=torch.float64, device="cuda")
