@@ -324,6 +324,95 @@ int8mm_status int8mm_outlier_columns_noalloc(const void* X_fp16_dev, int64_t M, 
  * freed handle is a no-op. */
 void int8mm_free(int8mm_weight_t h);
 
+/* ------------------------------------------------------------------------
+ * e4m3 products with block scales.
+ *
+ * The same place in a model as the decomposed matmul, for weights that are
+ * held as 8-bit floating point (e4m3: 4 exponent bits, 3 mantissa bits,
+ * largest number 448) with one fp32 scale for each block of 128 x 128, and
+ * activations with one for each group of 128 columns of a row:
+ *
+ *   Y[m,n] = sum_g sx[g][m] sw[n/128][g] sum_{k in g} xq[m,k] wq[n,k] (+ b[n])
+ *
+ * with g the groups of 128 of K (the last may be short), every sum in fp32
+ * and one rounding to 16 bits.  A value is code * scale.  Quantising a group
+ * (or a block) takes a = max |x| over it, raised to 2^-100 if smaller and not
+ * 0, scale = a / 448 and code = e4m3(x * (448 / a)), rounded to nearest, ties
+ * to even, the quotients and the product in fp32; a = 0 gives scale 0 and
+ * codes 0.  A group that holds Inf or NaN gets a scale of Inf or NaN and a
+ * NaN code, so every output of a product that reads it is NaN.  A sum past
+ * fp16's range becomes Inf.
+ *
+ * Layouts: activation codes [M, K] row-major; activation scales group-major,
+ * sx[g][m] at scales[g * lds + m] with lds >= M a multiple of 4 (the rows of
+ * all ceil(K/128) groups are lds long; entries past M are neither read into a
+ * result nor written); weight codes [N, K] row-major; weight scales
+ * [ceil(N/128)][ceil(K/128)].  K and N are multiples of 16, K at most
+ * INT8MM_MAX_K; 0 <= M < 2^31, M == 0 is a no-op.  16-bit data is fp16 or
+ * bf16 by `dtype`, one type per call.  Pointers are 16-byte aligned.
+ *
+ * Besides the weight a call uses only the caller's buffers: calls on several
+ * streams, threads or captured graphs may share a handle.  Outputs may not
+ * overlap inputs or each other unless the comment says so.  No call
+ * allocates except the two prepare calls; none synchronises except
+ * int8mm_block_get_status and int8mm_block_free.
+ * ---------------------------------------------------------------------- */
+typedef struct int8mm_block_weight* int8mm_block_weight_t; /* opaque, owned by the library */
+
+#define INT8MM_DTYPE_FP16 0
+#define INT8MM_DTYPE_BF16 1
+
+/* Quantise a 16-bit weight W [K, N] (row-major, as int8mm_prepare_weight
+ * takes it).  W is not kept: it may be freed once `stream` has passed the
+ * call. */
+int8mm_status int8mm_block_prepare_weight(const void* W_dev, int dtype, int64_t K, int64_t N, void* stream,
+                                          int8mm_block_weight_t* out);
+
+/* A weight whose codes [N, K] and scales [ceil(N/128)][ceil(K/128)] are given
+ * (a checkpoint's; the scale multiplies the code).  Neither is kept. */
+int8mm_status int8mm_block_prepare_codes(const void* codes_dev, const float* scales_dev, int64_t K, int64_t N,
+                                         void* stream, int8mm_block_weight_t* out);
+
+/* The handle's codes [N, K] and scales, read back (either may be NULL). */
+int8mm_status int8mm_block_weight_codes(int8mm_block_weight_t h, void* codes_dev, float* scales_dev, void* stream);
+
+/* Quantise the rows of X [M, K], ldx elements apart (a multiple of 8, >= K). */
+int8mm_status int8mm_block_quantize(const void* X_dev, int dtype, int64_t M, int64_t K, int64_t ldx, void* codes_dev,
+                                    float* scales_dev, int64_t lds, void* stream);
+
+/*
+ * Root-mean-square norm, with the residual's addition in front and 8-bit
+ * output behind:
+ *
+ *   h = round16(x + residual)   (x itself when residual is NULL)
+ *   y = h / sqrt(mean(h^2) + eps) * weight          (fp32)
+ *   residual_out = h;  normed = round16(y);  codes, scales = quantised y
+ *
+ * X and residual: rows ldx and ldr elements apart.  weight [K].
+ * residual_out [M, K]: NULL exactly when residual is; may be X or residual
+ * itself (same pointer, row stride K).  normed [M, K] and codes + scales:
+ * each may be NULL, not both; normed feeds layers that take 16-bit
+ * activations, such as int8mm_forward.  The codes come from y in fp32, not
+ * from its 16-bit rounding.  eps must be finite and >= 0.
+ */
+int8mm_status int8mm_block_rms_norm(const void* X_dev, int64_t ldx, const void* residual_dev, int64_t ldr,
+                                    const void* weight_dev, int dtype, int64_t M, int64_t K, float eps,
+                                    void* residual_out_dev, void* normed_dev, void* codes_dev, float* scales_dev,
+                                    int64_t lds, void* stream);
+
+/* Y [M, N] of type `dtype` from activation codes and scales; bias [N] of the
+ * same type, or NULL. */
+int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev, const float* scales_dev, int64_t lds,
+                                  int64_t M, const void* bias_dev, void* Y_dev, int dtype, void* stream);
+
+/* As int8mm_get_status, int8mm_set_wait_limit, int8mm_weight_bytes and
+ * int8mm_free, for a block-scaled weight.  A product that timed out leaves
+ * nothing behind that a later one reads: only its own Y is invalid. */
+int8mm_status int8mm_block_get_status(int8mm_block_weight_t h);
+int8mm_status int8mm_block_set_wait_limit(int8mm_block_weight_t h, uint64_t timeout_ns);
+int8mm_status int8mm_block_weight_bytes(int8mm_block_weight_t h, size_t* bytes);
+void int8mm_block_free(int8mm_block_weight_t h);
+
 /* Message of the last error returned on this host thread ("" if none). */
 const char* int8mm_last_error(void);
 

@@ -54,6 +54,17 @@ SIGNATURES = {
     "int8mm_free": (None, [_P]),
     "int8mm_last_error": (ctypes.c_char_p, []),
     "int8mm_outlier_columns_noalloc": (_ST, [_P, _I64, _I64, ctypes.c_float, _P, _P, _P, _P]),
+    "int8mm_block_prepare_weight": (_ST, [_P, ctypes.c_int, _I64, _I64, _P, ctypes.POINTER(_P)]),
+    "int8mm_block_prepare_codes": (_ST, [_P, _P, _I64, _I64, _P, ctypes.POINTER(_P)]),
+    "int8mm_block_weight_codes": (_ST, [_P, _P, _P, _P]),
+    "int8mm_block_quantize": (_ST, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _I64, _P]),
+    "int8mm_block_rms_norm": (_ST, [_P, _I64, _P, _I64, _P, ctypes.c_int, _I64, _I64, ctypes.c_float,
+                                    _P, _P, _P, _P, _I64, _P]),
+    "int8mm_block_matmul": (_ST, [_P, _P, _P, _I64, _I64, _P, _P, ctypes.c_int, _P]),
+    "int8mm_block_get_status": (_ST, [_P]),
+    "int8mm_block_set_wait_limit": (_ST, [_P, ctypes.c_uint64]),
+    "int8mm_block_weight_bytes": (_ST, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "int8mm_block_free": (None, [_P]),
 }
 
 
@@ -316,3 +327,8 @@ def int8mm_free(w: Weight) -> None:
 
 
 from .linear import Linear8bitLt  # noqa: E402  (the layer over the functions above)
+from .block import (  # noqa: E402  (the e4m3 block-scaled path)
+    BlockWeight, LinearBlock8bit, RMSNormBlock8bit, int8mm_block_forward, int8mm_block_free,
+    int8mm_block_get_status, int8mm_block_matmul, int8mm_block_prepare_codes, int8mm_block_prepare_weight,
+    int8mm_block_quantize, int8mm_block_rms_norm, int8mm_block_set_wait_limit, int8mm_block_weight_bytes,
+    int8mm_block_weight_codes)

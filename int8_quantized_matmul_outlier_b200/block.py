@@ -1,0 +1,331 @@
+"""The e4m3 block-scaled path: functions over the C ABI and two layers.
+
+Activations are e4m3 codes [M, K] with one fp32 scale per 128 columns of a
+row, weights e4m3 codes with one per 128 x 128 block; formulas, roundings and
+edge rules are in ``include/int8mm.h``.  ``scales`` of activations is indexed
+[M, G], G = ceil(K / 128), and stored group-major: strides (1, lds) with lds a
+multiple of 4, as ``int8mm_block_quantize`` and ``int8mm_block_rms_norm``
+return it.
+
+Argument marshalling only, as in the package's other functions.  Work goes to
+``stream``, or to the current stream of the arguments' device.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import sys
+
+import torch
+
+from . import _P, _check, lib
+
+_pkg = sys.modules[__package__]
+GROUP = 128
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _groups(k: int) -> int:
+    return -(-k // GROUP)
+
+
+class _On:
+    """The device of a call made current, and the raw handle of its stream."""
+
+    __slots__ = ("raw", "_ctx")
+
+    def __init__(self, device: torch.device, stream):
+        self._ctx = None
+        if torch.cuda.current_device() != device.index or stream is not None:
+            self._ctx = contextlib.ExitStack()
+            self._ctx.enter_context(torch.cuda.device(device))
+            if stream is not None:
+                if isinstance(stream, int):
+                    stream = torch.cuda.ExternalStream(stream, device=device)
+                if stream.device != device:
+                    self._ctx.close()
+                    raise ValueError(f"stream on {stream.device}, arguments on {device}")
+                # outputs allocated here belong to the stream that writes them
+                self._ctx.enter_context(torch.cuda.stream(stream))
+
+    def __enter__(self) -> int:
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.close()
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name} must be float16 or bfloat16")
+    return d
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> torch.Tensor:
+    """A 2-D 16-bit CUDA tensor whose rows are contiguous (any row stride)."""
+    if not (t.is_cuda and t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1)):
+        raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
+    _dtype(t, name)
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape or t.device != like.device):
+        raise ValueError(f"{name} must have the shape, type and device of its companion")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride; with one row any value will do, so the row's length."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _out(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _new_scales(M: int, G: int, device) -> torch.Tensor:
+    return torch.empty((G, (M + 3) // 4 * 4), dtype=torch.float32, device=device).t()[:M]
+
+
+def _scales_ld(s: torch.Tensor, M: int, G: int, device) -> int:
+    """The distance between the groups of scales [M, G]."""
+    if s.dtype != torch.float32 or tuple(s.shape) != (M, G) or s.device != device:
+        raise ValueError(f"scales must be float32 of shape ({M}, {G}) on {device}")
+    if M == 0:
+        return 4
+    lds = s.stride(1) if G > 1 else max(s.stride(1), (M + 3) // 4 * 4)
+    if (M > 1 and s.stride(0) != 1) or lds < M or lds % 4 != 0:
+        raise ValueError("scales must be stored group-major: strides (1, lds), lds >= M a multiple of 4, "
+                         "as int8mm_block_quantize returns it")
+    if (s.storage_offset() + (G - 1) * lds + (M + 3) // 4 * 4) * 4 > s.untyped_storage().nbytes():
+        raise ValueError("the storage of scales must hold whole groups (M rounded up to a multiple of 4)")
+    return lds
+
+
+class BlockWeight:
+    """A prepared e4m3 weight with block scales (the library-owned handle)."""
+
+    def __init__(self, handle: int, K: int, N: int, device: torch.device):
+        self.handle = handle
+        self.K, self.N = K, N
+        self.device = device
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _pkg is not None and _pkg._lib is not None:  # at exit the module may be gone first
+            _pkg._lib.int8mm_block_free(h)
+
+
+def int8mm_block_prepare_weight(W: torch.Tensor, stream=None) -> BlockWeight:
+    """Quantise a 16-bit weight W [K, N]; W is not kept."""
+    if not (W.is_cuda and W.dim() == 2 and W.is_contiguous()):
+        raise ValueError("W must be a contiguous 2-D CUDA tensor")
+    dtype, out = _dtype(W, "W"), _P()
+    K, N = W.shape
+    with _On(W.device, stream) as s:
+        _check(lib().int8mm_block_prepare_weight(W.data_ptr(), dtype, K, N, s, ctypes.byref(out)))
+    return BlockWeight(out.value, K, N, W.device)
+
+
+def int8mm_block_prepare_codes(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> BlockWeight:
+    """A weight whose e4m3 codes [N, K] and scales [ceil(N/128), ceil(K/128)]
+    (code * scale is the value) are at hand; neither is kept."""
+    if not (codes.is_cuda and codes.dim() == 2 and codes.is_contiguous() and codes.dtype == torch.float8_e4m3fn):
+        raise ValueError("codes must be a contiguous 2-D float8_e4m3fn CUDA tensor")
+    N, K = codes.shape
+    if (scales.dtype != torch.float32 or tuple(scales.shape) != (_groups(N), _groups(K))
+            or scales.device != codes.device or not scales.is_contiguous()):
+        raise ValueError(f"scales must be a contiguous float32 tensor [{_groups(N)}, {_groups(K)}] on codes' device")
+    out = _P()
+    with _On(codes.device, stream) as s:
+        _check(lib().int8mm_block_prepare_codes(codes.data_ptr(), scales.data_ptr(), K, N, s, ctypes.byref(out)))
+    return BlockWeight(out.value, K, N, codes.device)
+
+
+def int8mm_block_weight_codes(w: BlockWeight, stream=None):
+    """(codes [N, K] float8_e4m3fn, scales [ceil(N/128), ceil(K/128)] fp32) of a prepared weight."""
+    with _On(w.device, stream) as s:
+        codes = torch.empty((w.N, w.K), dtype=torch.float8_e4m3fn, device=w.device)
+        scales = torch.empty((_groups(w.N), _groups(w.K)), dtype=torch.float32, device=w.device)
+        _check(lib().int8mm_block_weight_codes(w.handle, codes.data_ptr(), scales.data_ptr(), s))
+    return codes, scales
+
+
+def int8mm_block_quantize(X: torch.Tensor, stream=None):
+    """(codes [M, K] float8_e4m3fn, scales [M, G]) of 16-bit rows X [M, K]
+    (rows contiguous, 16-byte aligned, any row stride)."""
+    _rows(X, "X")
+    M, K = X.shape
+    with _On(X.device, stream) as s:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+        scales = _new_scales(M, _groups(K), X.device)
+        _check(lib().int8mm_block_quantize(X.data_ptr(), _DTYPES[X.dtype], M, K, _ld(X), codes.data_ptr(),
+                                           scales.data_ptr(), scales.stride(1), s))
+    return codes, scales
+
+
+def int8mm_block_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                          residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                          codes: bool = True, normed: bool = False, stream=None):
+    """Root-mean-square norm of X + residual, quantised: returns (codes [M, K],
+    scales [M, G], residual_out [M, K], normed [M, K]), None for what is not
+    asked for (``codes=False`` leaves out codes and scales, ``normed`` is the
+    16-bit output) or has no residual.  ``residual_out`` may be ``residual`` or
+    ``X`` itself, which is then updated in place."""
+    _rows(X, "X")
+    M, K = X.shape
+    if (not weight.is_cuda or weight.dtype != X.dtype or weight.numel() != K or weight.dim() != 1
+            or not weight.is_contiguous() or weight.device != X.device):
+        raise ValueError("weight must be a contiguous tensor of K elements of X's type on X's device")
+    if residual is not None:
+        _rows(residual, "residual", X)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if not (codes or normed):
+        raise ValueError("neither codes nor the 16-bit output is asked for")
+    with _On(X.device, stream) as s:
+        ro = None if residual is None else _out(residual_out, "residual_out", (M, K), X.dtype, X.device)
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device) if codes else None
+        sc = _new_scales(M, _groups(K), X.device) if codes else None
+        y = torch.empty((M, K), dtype=X.dtype, device=X.device) if normed else None
+        _check(lib().int8mm_block_rms_norm(
+            X.data_ptr(), _ld(X), None if residual is None else residual.data_ptr(),
+            K if residual is None else _ld(residual), weight.data_ptr(), _DTYPES[X.dtype], M, K, float(eps),
+            None if ro is None else ro.data_ptr(), None if y is None else y.data_ptr(),
+            None if q is None else q.data_ptr(), None if sc is None else sc.data_ptr(),
+            (M + 3) // 4 * 4 if sc is None else sc.stride(1), s))
+    return q, sc, ro, y
+
+
+def _bias_ptr(bias: torch.Tensor | None, w: BlockWeight, dtype: torch.dtype):
+    if bias is None:
+        return None
+    if bias.dtype != dtype or bias.numel() != w.N or not bias.is_contiguous() or bias.device != w.device:
+        raise ValueError("bias must be a contiguous tensor of N elements of Y's type on the weight's device")
+    return bias.data_ptr()
+
+
+def int8mm_block_matmul(w: BlockWeight, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
+                        Y: torch.Tensor | None = None, dtype: torch.dtype = torch.float16, stream=None) -> torch.Tensor:
+    """Y [M, N] from activation codes [M, K] and scales [M, G]; ``dtype``
+    (float16 or bfloat16) is Y's and the bias's type."""
+    if not (codes.is_cuda and codes.dim() == 2 and codes.is_contiguous() and codes.dtype == torch.float8_e4m3fn):
+        raise ValueError("codes must be a contiguous 2-D float8_e4m3fn CUDA tensor")
+    M = codes.shape[0]
+    if codes.shape[1] != w.K:
+        raise ValueError(f"codes has {codes.shape[1]} columns, the weight has K={w.K}")
+    if codes.device != w.device:
+        raise ValueError(f"codes on {codes.device}, the weight on {w.device}")
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float16 or bfloat16")
+    lds = _scales_ld(scales, M, _groups(w.K), codes.device)
+    b = _bias_ptr(bias, w, dtype)
+    with _On(codes.device, stream) as s:
+        Y = _out(Y, "Y", (M, w.N), dtype, codes.device)
+        _check(lib().int8mm_block_matmul(w.handle, codes.data_ptr(), scales.data_ptr(), lds, M, b, Y.data_ptr(),
+                                         _DTYPES[dtype], s))
+    return Y
+
+
+def int8mm_block_forward(w: BlockWeight, X: torch.Tensor, bias: torch.Tensor | None = None,
+                         Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Quantise 16-bit rows X [M, K] and multiply: Y [M, N] of X's type, the
+    same as int8mm_block_quantize followed by int8mm_block_matmul."""
+    _rows(X, "X")
+    if X.shape[1] != w.K:
+        raise ValueError(f"X has {X.shape[1]} columns, the weight has K={w.K}")
+    if X.device != w.device:
+        raise ValueError(f"X on {X.device}, the weight on {w.device}")
+    codes, scales = int8mm_block_quantize(X, stream=stream)
+    return int8mm_block_matmul(w, codes, scales, bias=bias, Y=Y, dtype=X.dtype, stream=stream)
+
+
+def int8mm_block_get_status(w: BlockWeight) -> int:
+    """Synchronises the device; returns the status code (does not raise)."""
+    return int(lib().int8mm_block_get_status(w.handle))
+
+
+def int8mm_block_set_wait_limit(w: BlockWeight, timeout_ns: int) -> None:
+    """Limit of each device-side wait, in ns (at least 1e6)."""
+    _check(lib().int8mm_block_set_wait_limit(w.handle, int(timeout_ns)))
+
+
+def int8mm_block_weight_bytes(w: BlockWeight) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().int8mm_block_weight_bytes(w.handle, ctypes.byref(n)))
+    return int(n.value)
+
+
+def int8mm_block_free(w: BlockWeight) -> None:
+    h, w.handle = w.handle, None
+    if h:
+        lib().int8mm_block_free(h)
+
+
+class LinearBlock8bit(torch.nn.Module):
+    """y = x W + b with an e4m3 block-scaled weight, for inference.
+
+    x is fp16 or bf16 [..., in_features], or a pair (codes, scales) as
+    ``RMSNormBlock8bit`` and ``int8mm_block_quantize`` give it (the output is
+    then of ``dtype``).  The 16-bit weight is not kept."""
+
+    def __init__(self, weight: BlockWeight, bias: torch.Tensor | None = None, dtype: torch.dtype = torch.float16):
+        super().__init__()
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float16 or bfloat16")
+        self.in_features, self.out_features = weight.K, weight.N
+        self.dtype = dtype
+        self._w = weight
+        self.bias = None if bias is None else torch.nn.Parameter(bias.to(dtype), requires_grad=False)
+
+    @classmethod
+    def from_linear(cls, linear: torch.nn.Linear) -> "LinearBlock8bit":
+        """The layer of an ``nn.Linear`` in fp16 or bf16 (whose weight is [out, in])."""
+        with torch.no_grad():
+            w = int8mm_block_prepare_weight(linear.weight.detach().t().contiguous())
+            b = None if linear.bias is None else linear.bias.detach().clone()
+        return cls(w, b, linear.weight.dtype)
+
+    def forward(self, x) -> torch.Tensor:
+        if isinstance(x, tuple):
+            codes, scales = x
+            return int8mm_block_matmul(self._w, codes, scales, bias=self._bias(self.dtype), dtype=self.dtype)
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"last dimension {x.shape[-1]} != in_features {self.in_features}")
+        y = int8mm_block_forward(self._w, x.reshape(-1, self.in_features), bias=self._bias(x.dtype))
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def _bias(self, dtype):
+        if self.bias is not None and self.bias.dtype != dtype:
+            raise TypeError(f"activations of {dtype} with a bias of {self.bias.dtype}")
+        return None if self.bias is None else self.bias.data
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
+
+
+class RMSNormBlock8bit(torch.nn.Module):
+    """Root-mean-square norm whose output is the (codes, scales) pair that
+    ``LinearBlock8bit`` takes, for inference.
+
+    ``forward(x)`` returns the pair; ``forward(x, residual)`` returns (pair, x +
+    residual)."""
+
+    def __init__(self, dim: int, eps: float = 1e-6, dtype: torch.dtype = torch.float16, device=None):
+        super().__init__()
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float16 or bfloat16")
+        self.eps = float(eps)
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        self.weight = torch.nn.Parameter(torch.ones(dim, dtype=dtype, device=dev), requires_grad=False)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        dim = self.weight.numel()
+        if x.shape[-1] != dim:
+            raise ValueError(f"last dimension {x.shape[-1]} != {dim}")
+        r = None if residual is None else residual.reshape(-1, dim)
+        codes, scales, out, _ = int8mm_block_rms_norm(x.reshape(-1, dim), self.weight.data, self.eps, residual=r)
+        return (codes, scales) if residual is None else ((codes, scales), out.reshape(x.shape))

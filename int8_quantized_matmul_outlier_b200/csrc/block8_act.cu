@@ -1,0 +1,178 @@
+// Producers of e4m3 activations: the quantiser of 16-bit rows and the
+// root-mean-square norm with the residual's addition (formulas in block8.cuh
+// and at the kernels).  Both are bound by memory: every value is read once
+// into registers and every output written once from there.
+#include "block8.cuh"
+
+#include <algorithm>
+
+namespace i8mm {
+namespace {
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = pair_to_float<T>(w[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(float_to_pair<T>(v[0], v[1]), float_to_pair<T>(v[2], v[3]), float_to_pair<T>(v[4], v[5]),
+                    float_to_pair<T>(v[6], v[7]));
+}
+
+// Maximum over the 16 lanes that hold a group.
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// ------------------------------------------------------------- quantiser
+// 16 lanes per group, 8 values per lane; the groups of all rows are one list.
+constexpr int Q_THREADS = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(Q_THREADS) block_quantize_kernel(const BlockRowArgs a) {
+  const int64_t G = (a.K + kGroup - 1) / kGroup;
+  const int64_t total = a.M * G;
+  const int sub = threadIdx.x & 15;
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (Q_THREADS / 16); u0 < total;
+       u0 += static_cast<int64_t>(gridDim.x) * (Q_THREADS / 16)) {
+    const int64_t u = u0 + (threadIdx.x >> 4);
+    const int64_t row = u / G, g = u - row * G;
+    const int64_t col = g * kGroup + sub * 8;
+    const bool in = u < total && col < a.K;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in) unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + row * a.ldx + col), v);
+    float s, r;
+    group_scale(max16(absmax_bits8(v)), s, r);
+    if (in) *reinterpret_cast<uint2*>(a.codes + row * a.K + col) = e4m3_of8(v, r);
+    if (sub == 0 && u < total) a.scales[g * a.lds + row] = s;
+  }
+}
+
+// ------------------------------------------------------------------ norm
+//   h = round16(x + residual)          (x itself without a residual)
+//   y = h / sqrt(mean(h^2) + eps) * weight
+// then residual_out = h, normed = round16(y), codes and scales of y (from
+// fp32, not from its 16-bit rounding).  h is rounded before the norm because
+// it is what the residual stream holds: the norm of residual_out alone gives
+// the same y.  TPR threads hold a row in registers, VPT vectors of 8 values
+// each; the sum of squares is fp32, in a fixed order.
+template <typename T, int TPR, int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowArgs a) {
+  constexpr int ROWS = THREADS / TPR, WPR = TPR / 32;
+  __shared__ float part[THREADS / 32];
+  const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + rl;
+  const bool row_ok = row < a.M;
+  const int nvec = static_cast<int>(a.K >> 3);
+  uint4 h[VPT];
+  float sq = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = t + j * TPR;
+    h[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (row_ok && c < nvec) h[j] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + row * a.ldx)[c];
+  }
+  if (a.residual != nullptr) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = t + j * TPR;
+      if (row_ok && c < nvec) {
+        const uint4 ru = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + row * a.ldr)[c];
+        float x[8], r[8];
+        unpack8<T>(h[j], x);
+        unpack8<T>(ru, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], r[i]);
+        h[j] = pack8<T>(x);
+        reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.K)[c] = h[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float x[8];
+    unpack8<T>(h[j], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = __fmaf_rn(x[i], x[i], sq);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sq;
+    __syncthreads();
+    sq = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) sq += part[rl * WPR + w];
+  }
+  const float inv = __frsqrt_rn(__fadd_rn(__fdiv_rn(sq, static_cast<float>(a.K)), a.eps));
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = t + j * TPR;
+    if (j * TPR >= nvec) break;  // the same for every thread
+    const bool in = row_ok && c < nvec;
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in) {
+      float w[8];
+      unpack8<T>(h[j], y);
+      unpack8<T>(__ldg(reinterpret_cast<const uint4*>(a.weight) + c), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fmul_rn(y[i], inv), w[i]);
+      if (a.normed != nullptr) reinterpret_cast<uint4*>(static_cast<T*>(a.normed) + row * a.K)[c] = pack8<T>(y);
+    }
+    if (a.codes != nullptr) {
+      float s, r;
+      group_scale(max16(absmax_bits8(y)), s, r);
+      if (in) {
+        reinterpret_cast<uint2*>(a.codes + row * a.K)[c] = e4m3_of8(y, r);
+        if ((t & 15) == 0) a.scales[static_cast<int64_t>(c >> 4) * a.lds + row] = s;
+      }
+    }
+  }
+}
+
+template <typename T, int TPR, int VPT>
+cudaError_t norm_t(const BlockRowArgs& a, cudaStream_t stream) {
+  constexpr int THREADS = TPR < 128 ? 128 : TPR;
+  constexpr int ROWS = THREADS / TPR;
+  block_rms_norm_kernel<T, TPR, VPT, THREADS>
+      <<<static_cast<unsigned>((a.M + ROWS - 1) / ROWS), THREADS, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t norm_d(const BlockRowArgs& a, cudaStream_t stream) {
+  const int64_t nvec = a.K / 8;
+  if (nvec <= 32) return norm_t<T, 32, 1>(a, stream);
+  if (nvec <= 128) return norm_t<T, 32, 4>(a, stream);
+  if (nvec <= 512) return norm_t<T, 128, 4>(a, stream);
+  if (nvec <= 1024) return norm_t<T, 256, 4>(a, stream);
+  if (nvec <= 2048) return norm_t<T, 512, 4>(a, stream);
+  if (nvec <= 4096) return norm_t<T, 1024, 4>(a, stream);
+  return norm_t<T, 1024, 8>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_block_quantize(const BlockRowArgs& a, int dtype, int num_sms, cudaStream_t stream) {
+  const int64_t units = a.M * block_groups(a.K);
+  const int64_t blocks = (units + Q_THREADS / 16 - 1) / (Q_THREADS / 16);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * 64));
+  if (dtype == kDtypeBf16) block_quantize_kernel<__nv_bfloat16><<<grid, Q_THREADS, 0, stream>>>(a);
+  else block_quantize_kernel<__half><<<grid, Q_THREADS, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_block_rms_norm(const BlockRowArgs& a, int dtype, int num_sms, cudaStream_t stream) {
+  (void)num_sms;
+  return dtype == kDtypeBf16 ? norm_d<__nv_bfloat16>(a, stream) : norm_d<__half>(a, stream);
+}
+
+}  // namespace i8mm

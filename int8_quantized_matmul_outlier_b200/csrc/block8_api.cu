@@ -1,0 +1,395 @@
+// C ABI of the e4m3 block-scaled path (declared in include/int8mm.h): weight
+// handles, argument checks and launches.  A handle holds the weight, its
+// scales and a status word; every other buffer is the caller's, so calls on
+// different streams and captured graphs share no workspace.
+#include "block8.cuh"
+#include "block8_gemm.cuh"
+#include "int8mm.h"
+#include "kernels.cuh"
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <initializer_list>
+#include <mutex>
+#include <new>
+#include <string>
+#include <unordered_set>
+
+using namespace i8mm;
+
+struct int8mm_block_weight {
+  int device = 0;
+  int num_sms = 148;
+  int64_t K = 0, N = 0, N_pad = 0;
+  uint8_t* Wb = nullptr;  // [G][N_pad][128] codes
+  float* sw = nullptr;    // [N / 128][G]
+  int* status = nullptr;
+  unsigned long long timeout_ns = 2000000000ull;
+  size_t bytes = 0;
+};
+
+namespace {
+
+std::mutex g_mu;
+std::unordered_set<const int8mm_block_weight*> g_live;
+
+int8mm_status fail(int8mm_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int8mm_status fail(int8mm_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  set_last_error(buf);
+  return s;
+}
+
+int8mm_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(e == cudaErrorMemoryAllocation ? INT8MM_ERR_OOM : INT8MM_ERR_CUDA, "%s: %s (%s)", what,
+              cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+bool live(const int8mm_block_weight* h) {
+  std::lock_guard<std::mutex> g(g_mu);
+  return h != nullptr && g_live.count(h) != 0;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Makes a handle's device current for a call and puts the caller's back.
+struct DeviceGuard {
+  int prev = -1;
+  cudaError_t err = cudaSuccess;
+  explicit DeviceGuard(int dev) {
+    err = cudaGetDevice(&prev);
+    if (err == cudaSuccess && prev != dev) err = cudaSetDevice(dev);
+    else prev = -1;
+  }
+  ~DeviceGuard() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
+int sm_count() {
+  static int cached[64] = {};
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return n;
+  if (dev < 64 && cached[dev] > 0) return cached[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+  if (dev < 64) cached[dev] = n;
+  return n;
+}
+
+int8mm_status check_dtype(int dtype) {
+  if (dtype != INT8MM_DTYPE_FP16 && dtype != INT8MM_DTYPE_BF16)
+    return fail(INT8MM_ERR_INVALID_ARG, "dtype %d: need INT8MM_DTYPE_FP16 or INT8MM_DTYPE_BF16", dtype);
+  return INT8MM_OK;
+}
+
+int8mm_status check_k(int64_t K) {
+  if (K < 16 || K % 16 != 0 || K > kBlockMaxK)
+    return fail(INT8MM_ERR_UNSUPPORTED_SHAPE, "K=%lld: need a multiple of 16 in 16 .. %lld", (long long)K,
+                (long long)kBlockMaxK);
+  return INT8MM_OK;
+}
+
+int8mm_status check_m(int64_t M) {
+  if (M < 0 || M >= (int64_t(1) << 31)) return fail(INT8MM_ERR_INVALID_ARG, "M=%lld out of range", (long long)M);
+  return INT8MM_OK;
+}
+
+// Rows of 16-bit values, ld apart.
+int8mm_status check_rows(const char* name, const void* p, int64_t ld, int64_t K) {
+  if (p == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < K || ld >= (int64_t(1) << 31))
+    return fail(INT8MM_ERR_INVALID_ARG, "%s: row stride %lld with K=%lld", name, (long long)ld, (long long)K);
+  if (!aligned16(p) || ld % 8 != 0)
+    return fail(INT8MM_ERR_ALIGNMENT, "%s: rows must be 16-byte aligned (row stride %lld)", name, (long long)ld);
+  return INT8MM_OK;
+}
+
+int8mm_status check_scales(const float* scales, int64_t lds, int64_t M) {
+  if (scales == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "scales is NULL");
+  if (lds < M || lds % 4 != 0 || lds >= (int64_t(1) << 31))
+    return fail(INT8MM_ERR_INVALID_ARG, "scales: stride %lld between groups; need a multiple of 4 that is >= M=%lld",
+                (long long)lds, (long long)M);
+  if (!aligned16(scales)) return fail(INT8MM_ERR_ALIGNMENT, "scales must be 16-byte aligned");
+  return INT8MM_OK;
+}
+
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr) return false;
+  const auto pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  return pa < pb + b.bytes && pb < pa + a.bytes;
+}
+int8mm_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return fail(INT8MM_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
+    for (auto q = outs.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return fail(INT8MM_ERR_INVALID_ARG, "%s overlaps %s", o->name, q->name);
+  }
+  return INT8MM_OK;
+}
+size_t rows_bytes(int64_t M, int64_t K, int64_t ld, size_t elem) {
+  return static_cast<size_t>((M - 1) * ld + K) * elem;
+}
+size_t scales_bytes(int64_t K, int64_t lds) { return static_cast<size_t>(block_groups(K) * lds) * 4; }
+
+void free_all(int8mm_block_weight* h) {
+  if (h->Wb) cudaFree(h->Wb);
+  if (h->sw) cudaFree(h->sw);
+  if (h->status) cudaFree(h->status);
+  delete h;
+}
+
+// Shared by the two ways to prepare a weight: from 16-bit W (scales NULL) or
+// from codes and scales.
+int8mm_status prepare(const void* W, int dtype, const float* scales, int64_t K, int64_t N, void* stream,
+                      int8mm_block_weight_t* out) {
+  if (out == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (W == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "W is NULL");
+  int8mm_status st = check_k(K);
+  if (st != INT8MM_OK) return st;
+  if (N < 16 || N % 16 != 0 || N >= (int64_t(1) << 31) - 256)
+    return fail(INT8MM_ERR_UNSUPPORTED_SHAPE, "N=%lld: need a multiple of 16, from 16", (long long)N);
+  const int64_t N_pad = (N + kWeightRowPad - 1) / kWeightRowPad * kWeightRowPad;
+  const int64_t G = block_groups(K);
+  if (G * N_pad >= (int64_t(1) << 31))
+    return fail(INT8MM_ERR_UNSUPPORTED_SHAPE, "K=%lld x N=%lld exceeds the weight layout's 2^31 rows of 128 bytes",
+                (long long)K, (long long)N);
+  if (!aligned16(W)) return fail(INT8MM_ERR_ALIGNMENT, "W must be 16-byte aligned");
+  int8mm_block_weight* h = new (std::nothrow) int8mm_block_weight();
+  if (h == nullptr) return fail(INT8MM_ERR_OOM, "host allocation");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaGetDevice(&h->device);
+  h->num_sms = sm_count();
+  h->K = K;
+  h->N = N;
+  h->N_pad = N_pad;
+  const size_t nsw = static_cast<size_t>((N + kGroup - 1) / kGroup * G);
+  const size_t nwb = static_cast<size_t>(G * N_pad) * kGroup;
+  if (e == cudaSuccess) e = cudaMallocAsync(reinterpret_cast<void**>(&h->Wb), nwb, s);
+  if (e == cudaSuccess) e = cudaMallocAsync(reinterpret_cast<void**>(&h->sw), nsw * 4, s);
+  if (e == cudaSuccess) e = cudaMallocAsync(reinterpret_cast<void**>(&h->status), 4, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, 4, s);
+  h->bytes = nwb + nsw * 4 + 4;
+  if (e == cudaSuccess) {
+    if (scales == nullptr) {
+      e = launch_block_weight_quantize(W, dtype, K, N, h->Wb, N_pad, h->sw, s);
+    } else {
+      e = cudaMemcpyAsync(h->sw, scales, nsw * 4, cudaMemcpyDeviceToDevice, s);
+      if (e == cudaSuccess) e = launch_block_weight_pack(static_cast<const uint8_t*>(W), K, N, h->Wb, N_pad, s);
+    }
+  }
+  if (e != cudaSuccess) {
+    cudaStreamSynchronize(s);
+    free_all(h);
+    return cuda_fail(e, "weight preparation");
+  }
+  {
+    std::lock_guard<std::mutex> g(g_mu);
+    g_live.insert(h);
+  }
+  *out = h;
+  return INT8MM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int8mm_status int8mm_block_prepare_weight(const void* W_dev, int dtype, int64_t K, int64_t N, void* stream,
+                                          int8mm_block_weight_t* out) {
+  if (out != nullptr) *out = nullptr;
+  int8mm_status st = check_dtype(dtype);
+  return st != INT8MM_OK ? st : prepare(W_dev, dtype, nullptr, K, N, stream, out);
+}
+
+int8mm_status int8mm_block_prepare_codes(const void* codes_dev, const float* scales_dev, int64_t K, int64_t N,
+                                         void* stream, int8mm_block_weight_t* out) {
+  if (out != nullptr) *out = nullptr;
+  if (scales_dev == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "scales is NULL");
+  return prepare(codes_dev, 0, scales_dev, K, N, stream, out);
+}
+
+int8mm_status int8mm_block_weight_codes(int8mm_block_weight_t h, void* codes_dev, float* scales_dev, void* stream) {
+  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+  if (codes_dev != nullptr && !aligned16(codes_dev)) return fail(INT8MM_ERR_ALIGNMENT, "codes must be 16-byte aligned");
+  DeviceGuard dg(h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = dg.err;
+  if (e == cudaSuccess && codes_dev != nullptr)
+    e = launch_block_weight_unpack(h->Wb, h->K, h->N, h->N_pad, static_cast<uint8_t*>(codes_dev), s);
+  if (e == cudaSuccess && scales_dev != nullptr)
+    e = cudaMemcpyAsync(scales_dev, h->sw, static_cast<size_t>((h->N + kGroup - 1) / kGroup * block_groups(h->K)) * 4,
+                        cudaMemcpyDeviceToDevice, s);
+  return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "weight read-back");
+}
+
+int8mm_status int8mm_block_quantize(const void* X_dev, int dtype, int64_t M, int64_t K, int64_t ldx, void* codes_dev,
+                                    float* scales_dev, int64_t lds, void* stream) {
+  int8mm_status st;
+  if ((st = check_dtype(dtype)) != INT8MM_OK || (st = check_k(K)) != INT8MM_OK || (st = check_m(M)) != INT8MM_OK)
+    return st;
+  if (M == 0) return INT8MM_OK;
+  if ((st = check_rows("X", X_dev, ldx, K)) != INT8MM_OK || (st = check_rows("codes", codes_dev, K, K)) != INT8MM_OK ||
+      (st = check_scales(scales_dev, lds, M)) != INT8MM_OK ||
+      (st = check_apart({{"codes", codes_dev, static_cast<size_t>(M * K)}, {"scales", scales_dev, scales_bytes(K, lds)}},
+                        {{"X", X_dev, rows_bytes(M, K, ldx, 2)}})) != INT8MM_OK)
+    return st;
+  BlockRowArgs a = {};
+  a.X = X_dev;
+  a.M = M;
+  a.K = K;
+  a.ldx = ldx;
+  a.codes = static_cast<uint8_t*>(codes_dev);
+  a.scales = scales_dev;
+  a.lds = lds;
+  const cudaError_t e = launch_block_quantize(a, dtype, sm_count(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "quantiser launch");
+}
+
+int8mm_status int8mm_block_rms_norm(const void* X_dev, int64_t ldx, const void* residual_dev, int64_t ldr,
+                                    const void* weight_dev, int dtype, int64_t M, int64_t K, float eps,
+                                    void* residual_out_dev, void* normed_dev, void* codes_dev, float* scales_dev,
+                                    int64_t lds, void* stream) {
+  int8mm_status st;
+  if ((st = check_dtype(dtype)) != INT8MM_OK || (st = check_k(K)) != INT8MM_OK || (st = check_m(M)) != INT8MM_OK)
+    return st;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(INT8MM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if ((residual_dev == nullptr) != (residual_out_dev == nullptr))
+    return fail(INT8MM_ERR_INVALID_ARG, "residual and residual_out go together");
+  if ((codes_dev == nullptr) != (scales_dev == nullptr))
+    return fail(INT8MM_ERR_INVALID_ARG, "codes and scales go together");
+  if (M == 0) return INT8MM_OK;
+  if (codes_dev == nullptr && normed_dev == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "no output is asked for");
+  const size_t out2 = static_cast<size_t>(M * K) * 2;
+  if ((st = check_rows("X", X_dev, ldx, K)) != INT8MM_OK || (st = check_rows("weight", weight_dev, K, K)) != INT8MM_OK)
+    return st;
+  if (residual_dev != nullptr && ((st = check_rows("residual", residual_dev, ldr, K)) != INT8MM_OK ||
+                                  (st = check_rows("residual_out", residual_out_dev, K, K)) != INT8MM_OK))
+    return st;
+  if (normed_dev != nullptr && (st = check_rows("normed", normed_dev, K, K)) != INT8MM_OK) return st;
+  if (codes_dev != nullptr && ((st = check_rows("codes", codes_dev, K, K)) != INT8MM_OK ||
+                               (st = check_scales(scales_dev, lds, M)) != INT8MM_OK))
+    return st;
+  const Span x = {"X", X_dev, rows_bytes(M, K, ldx, 2)}, w = {"weight", weight_dev, static_cast<size_t>(K) * 2};
+  const Span r = {"residual", residual_dev, residual_dev ? rows_bytes(M, K, ldr, 2) : 0};
+  const Span c = {"codes", codes_dev, static_cast<size_t>(M * K)};
+  const Span sc = {"scales", scales_dev, codes_dev ? scales_bytes(K, lds) : 0};
+  const Span no = {"normed", normed_dev, out2};
+  // residual_out may be X or residual in place: each value is read before
+  // the same thread writes it
+  const bool on_x = residual_out_dev != nullptr && residual_out_dev == X_dev && ldx == K;
+  const bool on_r = residual_out_dev != nullptr && residual_out_dev == residual_dev && ldr == K;
+  const Span none = {"", nullptr, 0};
+  if ((st = check_apart({c, sc, no}, {x, r, w})) != INT8MM_OK ||
+      (st = check_apart({{"residual_out", residual_out_dev, out2}}, {on_x ? none : x, on_r ? none : r, w, c, sc, no})) !=
+          INT8MM_OK)
+    return st;
+  BlockRowArgs a = {};
+  a.X = X_dev;
+  a.M = M;
+  a.K = K;
+  a.ldx = ldx;
+  a.residual = residual_dev;
+  a.ldr = ldr;
+  a.weight = weight_dev;
+  a.eps = eps;
+  a.residual_out = residual_out_dev;
+  a.normed = normed_dev;
+  a.codes = static_cast<uint8_t*>(codes_dev);
+  a.scales = scales_dev;
+  a.lds = lds;
+  const cudaError_t e = launch_block_rms_norm(a, dtype, sm_count(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "norm launch");
+}
+
+int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev, const float* scales_dev, int64_t lds,
+                                  int64_t M, const void* bias_dev, void* Y_dev, int dtype, void* stream) {
+  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+  int8mm_status st;
+  if ((st = check_dtype(dtype)) != INT8MM_OK || (st = check_m(M)) != INT8MM_OK) return st;
+  if (M == 0) return INT8MM_OK;
+  const int64_t K = h->K, N = h->N;
+  if ((st = check_rows("codes", codes_dev, K, K)) != INT8MM_OK ||
+      (st = check_scales(scales_dev, lds, M)) != INT8MM_OK || (st = check_rows("Y", Y_dev, N, N)) != INT8MM_OK)
+    return st;
+  if (bias_dev != nullptr && !aligned16(bias_dev)) return fail(INT8MM_ERR_ALIGNMENT, "bias must be 16-byte aligned");
+  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64);
+  if (tiles >= (int64_t(1) << 31))
+    return fail(INT8MM_ERR_UNSUPPORTED_SHAPE, "M=%lld x N=%lld is too large", (long long)M, (long long)N);
+  if ((st = check_apart({{"Y", Y_dev, static_cast<size_t>(M * N) * 2}},
+                        {{"codes", codes_dev, static_cast<size_t>(M * K)},
+                         {"scales", scales_dev, scales_bytes(K, lds)},
+                         {"bias", bias_dev, static_cast<size_t>(N) * 2}})) != INT8MM_OK)
+    return st;
+  DeviceGuard dg(h->device);
+  if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+  BlockGemmArgs a = {};
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.N_pad = static_cast<int>(h->N_pad);
+  a.X = static_cast<const uint8_t*>(codes_dev);
+  a.Wb = h->Wb;
+  a.sx = scales_dev;
+  a.lds = lds;
+  a.sw = h->sw;
+  a.bias = bias_dev;
+  a.Y = Y_dev;
+  a.bf16 = dtype == INT8MM_DTYPE_BF16;
+  a.status = h->status;
+  a.timeout_ns = h->timeout_ns;
+  const cudaError_t e = launch_block_gemm(a, h->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "block-scaled product launch");
+}
+
+int8mm_status int8mm_block_get_status(int8mm_block_weight_t h) {
+  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+  DeviceGuard dg(h->device);
+  cudaError_t e = dg.err;
+  int word = 0;
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&word, h->status, 4, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemset(h->status, 0, 4);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return cuda_fail(e, "status read");
+  return (word & kStatusTimeout) ? fail(INT8MM_ERR_TIMEOUT, "a device wait ran out of time") : INT8MM_OK;
+}
+
+int8mm_status int8mm_block_set_wait_limit(int8mm_block_weight_t h, uint64_t timeout_ns) {
+  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+  if (timeout_ns < 1000000ull)
+    return fail(INT8MM_ERR_INVALID_ARG, "timeout %llu ns is below the 1 ms minimum",
+                static_cast<unsigned long long>(timeout_ns));
+  h->timeout_ns = timeout_ns;
+  return INT8MM_OK;
+}
+
+int8mm_status int8mm_block_weight_bytes(int8mm_block_weight_t h, size_t* bytes) {
+  if (!live(h) || bytes == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid handle or NULL output");
+  *bytes = h->bytes;
+  return INT8MM_OK;
+}
+
+void int8mm_block_free(int8mm_block_weight_t h) {
+  if (h == nullptr) return;
+  {
+    std::lock_guard<std::mutex> g(g_mu);
+    if (g_live.erase(h) == 0) return;
+  }
+  DeviceGuard dg(h->device);
+  cudaDeviceSynchronize();
+  free_all(h);
+}
+
+}  // extern "C"
