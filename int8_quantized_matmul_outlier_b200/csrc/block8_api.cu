@@ -7,6 +7,10 @@
 #include "int8mm.h"
 #include "kernels.cuh"
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -97,6 +101,26 @@ int8mm_status check_k(int64_t K) {
 int8mm_status check_m(int64_t M) {
   if (M < 0 || M >= (int64_t(1) << 31)) return fail(INT8MM_ERR_INVALID_ARG, "M=%lld out of range", (long long)M);
   return INT8MM_OK;
+}
+
+// 2-D array of bytes [rows, inner] (inner contiguous), 128-byte swizzled boxes
+// of 128 bytes x box_rows, zero fill outside.
+int8mm_status make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? p : nullptr);
+  }();
+  if (fn == nullptr) return fail(INT8MM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner};
+  const cuuint32_t box[2] = {kGroup, box_rows}, estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? INT8MM_OK
+                           : fail(INT8MM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
 }
 
 // Rows of 16-bit values, ld apart.
@@ -324,8 +348,7 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
       (st = check_scales(scales_dev, lds, M)) != INT8MM_OK || (st = check_rows("Y", Y_dev, N, N)) != INT8MM_OK)
     return st;
   if (bias_dev != nullptr && !aligned16(bias_dev)) return fail(INT8MM_ERR_ALIGNMENT, "bias must be 16-byte aligned");
-  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64);
-  if (tiles >= (int64_t(1) << 31))
+  if (((M + 127) / 128) * ((N + 63) / 64) >= (int64_t(1) << 31))
     return fail(INT8MM_ERR_UNSUPPORTED_SHAPE, "M=%lld x N=%lld is too large", (long long)M, (long long)N);
   if ((st = check_apart({{"Y", Y_dev, static_cast<size_t>(M * N) * 2}},
                         {{"codes", codes_dev, static_cast<size_t>(M * K)},
@@ -349,7 +372,14 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
   a.bf16 = dtype == INT8MM_DTYPE_BF16;
   a.status = h->status;
   a.timeout_ns = h->timeout_ns;
-  const cudaError_t e = launch_block_gemm(a, h->num_sms, static_cast<cudaStream_t>(stream));
+  CUtensorMap tmX, tmW;
+  const int width = block_pair_width(M, N, h->num_sms);
+  if ((st = make_tmap(&tmX, codes_dev, static_cast<uint64_t>(K), static_cast<uint64_t>(M), 128)) != INT8MM_OK ||
+      (st = make_tmap(&tmW, h->Wb, kGroup, static_cast<uint64_t>(block_groups(K) * h->N_pad),
+                      static_cast<uint32_t>(width / 2))) != INT8MM_OK)
+    return st;
+  const cudaError_t e =
+      launch_block_gemm_pair(tmX, tmW, a, width, h->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "block-scaled product launch");
 }
 

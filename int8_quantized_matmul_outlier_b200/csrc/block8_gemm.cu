@@ -1,90 +1,407 @@
-// Matrix product of e4m3 codes with block scales:
-//   Y[m, n] = sum_g sx[g][m] sw[n / 128][g] sum_{k in g} X[m, k] W[n, k]  (+ bias[n])
-// fp32 sums, one rounding to 16 bits.  A plain tiled kernel on the CUDA
-// cores: 64 x 64 outputs per block, one group at a time in shared memory.
+// Matrix product of e4m3 codes with block scales for many rows, sm_100a:
+//
+//   Y[m, n] = sum_g sx[g][m] sw[n / 128][g] P_g[m, n]  (+ bias[n])
+//   P_g[m, n] = sum_{k in g} X[m, k] W[n, k]
+//
+// P_g comes from the tensor cores (tcgen05.mma kind::f8f6f4, fp32 sums).  Its
+// factor changes with every group of 128 columns of K and is any fp32 number,
+// so the sum over g cannot stay in the tensor cores' accumulator: P_g of each
+// group is read from TMEM and added to fp32 registers with its factor.
+//
+// Structure: clusters of two CTAs on neighbouring SMs (a CTA pair), one CTA
+// per SM, persistent over 256 x BN tiles.  Each CTA loads its own 128 rows of
+// X and BN / 2 rows of W per group (TMA, 128-byte swizzle, completing on the
+// leader's barrier), keeps its 128 rows of P_g in its own TMEM, sums and
+// writes them.  No multicast.
+//   warp 0      TMA producer
+//   warp 1      allocates TMEM; in the leader one thread issues 4 MMAs of
+//               256 x BN x 32 per group, alternating between two buffers
+//   warps 4-11  two per TMEM lane quarter, one row per thread and half of the
+//               tile's columns: they add P_g times sx sw to BN / 2 registers
+//               and write Y at the tile's end, while the next tile's first
+//               two groups already run
+// A group takes the tensor cores 2 BN cycles (BN = 256: 512); in that time
+// the eight warps read 128 x BN values (256 cycles of TMEM reads) and make as
+// many multiply-adds (256 cycles, two per packed instruction), so the sums
+// hide behind the tensor cores as long as a buffer is handed back within one
+// group's time.
+//
+// BN: the tile width is chosen from 256, 192 and 128 so that the tiles fill
+// the pairs' rounds (block_pair_width).  A 192-wide tile does not start on a
+// 128-column block of the weight scales, but its chunks of 32 columns never
+// cross one: a half-tile meets at most two blocks.
+//
+// Every wait is bounded; a timeout sets the status word and the CTA drains
+// and exits.
 #include "block8.cuh"
 #include "block8_gemm.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+#include <algorithm>
 
 namespace i8mm {
 namespace {
 
-constexpr int T = 64;
+constexpr int TILE_M = 256;
+constexpr int BM = 128;  // rows per CTA
+constexpr int EPI_WARPS = 8;
+// Three warpgroups, so that registers can move between them: launched with
+// 168 each (384 x 168 = 64512), the first (producer, MMA issuer, two idle
+// warps) goes down to 72 and the two epilogue groups up to 216
+// (128 x 72 + 256 x 216 = 64512).
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
+constexpr int REGS_LAUNCH = 168, REGS_FRONT = 72, REGS_EPI = 216;
+static_assert(128 * REGS_FRONT + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS_LAUNCH, "registers within the launch's");
 
-__device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&f)[4]) {
-  uint32_t lo, hi;
-  asm("{.reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-  const float2 x = pair_to_float<__half>(lo), y = pair_to_float<__half>(hi);
-  f[0] = x.x;
-  f[1] = x.y;
-  f[2] = y.x;
-  f[3] = y.y;
+template <int BN>
+struct PCfg {
+  static constexpr int A_BYTES = BM * kGroup;
+  static constexpr int B_BYTES = BN / 2 * kGroup;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 229376 / STAGE;
+  static constexpr int HALF = BN / 2;  // columns per epilogue warp
+  static constexpr int NBARS = 2 * STAGES + 5;
+  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + 1024;  // + slack to align the base to 1024
+  static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, BN);  // e4m3 and fp16 operands share the encoding 0
+  static_assert(HALF % 32 == 0 && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
+};
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
-template <typename TY>
-__global__ void __launch_bounds__(256) block_gemm_simple_kernel(const BlockGemmArgs a) {
-  __shared__ uint32_t xs[T][33], ws[T][33];
-  const int m0 = blockIdx.y * T, n0 = blockIdx.x * T;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+__device__ __forceinline__ void gfail(const BlockGemmArgs& a, volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(a.status, kStatusTimeout);
+}
+
+// acc (two fp32) += p (two fp32) * s (two fp32), each rounded once.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t p0, uint32_t p1, uint64_t s) {
+  asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(p0), "r"(p1), "l"(s));
+}
+__device__ __forceinline__ uint64_t twice(float s) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+template <int BN, typename TY>
+__global__ void __launch_bounds__(THREADS, 1)
+    block_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                           const BlockGemmArgs a) {
+  using C = PCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int M = a.M, N = a.N;
+  const uint32_t rank = cluster_ctarank();
+  const int tile0 = static_cast<int>(blockIdx.x) / 2;
+  const int tstride = static_cast<int>(gridDim.x) / 2;
+  const int num_m = (M + TILE_M - 1) / TILE_M;
+  const int num_tiles = num_m * ((N + BN - 1) / BN);
   const int G = (a.K + kGroup - 1) / kGroup;
-  float acc[4][4] = {};
-  for (int g = 0; g < G; ++g) {
-    for (int e = threadIdx.x; e < T * 32; e += 256) {
-      const int r = e >> 5, w = e & 31, k = g * kGroup + w * 4;
-      xs[r][w] = (m0 + r < a.M && k < a.K)
-                     ? *reinterpret_cast<const uint32_t*>(a.X + static_cast<size_t>(m0 + r) * a.K + k) : 0u;
-      ws[r][w] = n0 + r < a.N_pad
-                     ? *reinterpret_cast<const uint32_t*>(a.Wb + (static_cast<size_t>(g) * a.N_pad + n0 + r) * kGroup + w * 4)
-                     : 0u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    __syncthreads();
-    float part[4][4] = {};
-    for (int w = 0; w < 32; ++w) {
-      float x[4][4], y[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e4m3x4_to_float(xs[ty + 16 * i][w], x[i]);
-        e4m3x4_to_float(ws[tx + 16 * i][w], y[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) part[i][j] = fmaf(x[i][k], y[j][k], part[i][j]);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], EPI_WARPS * 2);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (m < a.M && n < a.N)
-          acc[i][j] = fmaf(part[i][j], a.sx[static_cast<size_t>(g) * a.lds + m] * a.sw[(n / kGroup) * G + g], acc[i][j]);
-      }
-    __syncthreads();
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m < a.M && n < a.N) {
-        float v = acc[i][j];
-        if (a.bias != nullptr) v += static_cast<float>(static_cast<const TY*>(a.bias)[n]);
-        static_cast<TY*>(a.Y)[static_cast<size_t>(m) * a.N + n] = TY(v);
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // the peer's barriers are initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const unsigned long long tmo = a.timeout_ns;
+
+  if (warp < 4) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FRONT));
+   if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+      bool ok = true;
+      const uint64_t pol_x = l2_policy_evict_last();  // every column tile of its rows reads X again
+      for (int t = tile0; t < num_tiles && ok; t += tstride) {
+        const int m0 = (t % num_m) * TILE_M + static_cast<int>(rank) * BM;
+        const int n0 = (t / num_m) * BN + static_cast<int>(rank) * (BN / 2);
+        for (int g = 0; g < G; ++g) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, tmo, abort_flag)) {
+            ok = false;
+            break;
+          }
+          // both CTAs' loads complete on the leader's barrier; the leader
+          // announces the pair's bytes
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE);
+          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          uint8_t* st = smem + stage * C::STAGE;
+          tma_load_2d_pair_hint(st, &tmX, bar, g * kGroup, m0, pol_x);
+          tma_load_2d_pair(st + C::A_BYTES, &tmW, bar, 0, g * a.N_pad + n0);
+          issued_mask |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        gfail(a, abort_flag);
+        // every load already issued lands before the CTA can exit (the peer
+        // cannot watch the leader's barriers: it waits a while)
+        if (rank == 0) {
+          for (int s = 0; s < C::STAGES; ++s)
+            if (issued_mask & (1u << s)) mbar_wait(&full[s], (issued_phase >> s) & 1u, tmo, nullptr);
+        } else {
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < 200000ull) {
+          }
+        }
       }
     }
+   } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // -------------------------------------------------------- MMA issuer
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      bool ok = true;
+      for (int t = tile0; t < num_tiles && ok; t += tstride) {
+        for (int g = 0; g < G; ++g, ++it) {
+          const uint32_t buf = it & 1u;
+          if (!mbar_wait(&tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag) ||
+              !mbar_wait(&full[stage], phase, tmo, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * C::STAGE);
+          const uint64_t adesc = smem_desc_k_sw128(sa);
+          const uint64_t bdesc = smem_desc_k_sw128(sa + C::A_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
+            mma_e4m3_pair(tmem_base + buf * 256u, adesc + static_cast<uint64_t>(kk * 2),
+                          bdesc + static_cast<uint64_t>(kk * 2), C::IDESC, kk != 0 ? 1u : 0u);
+          mma_commit_pair(&tfull[buf], 0x3);
+          mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        gfail(a, abort_flag);
+        mma_commit_pair(drain, 0x1);
+        mbar_wait(drain, 0, tmo, nullptr);
+      }
+    }
+   }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+    // ----------------------------------------------------- sums and epilogue
+    const int q = warp & 3;             // TMEM lane quarter this warp may read
+    const int h = (warp - 4) >> 2;      // half of the tile's columns
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    constexpr int CH = C::HALF / 32;
+    const int NB = (N + kGroup - 1) / kGroup;
+    uint32_t it = 0;
+    bool alive = true;
+    for (int t = tile0; t < num_tiles && alive; t += tstride) {
+      const int m = (t % num_m) * TILE_M + static_cast<int>(rank) * BM + q * 32 + lane;
+      const int nh = (t / num_m) * BN + h * C::HALF;
+      const bool row_ok = m < M;
+      // the scales: this row's, and those of the one or two weight blocks
+      // that the half-tile meets (past N: any block's, the sums are dropped)
+      const float* sxp = a.sx + (row_ok ? m : 0);
+      const int b0 = min(nh / kGroup, NB - 1), b1 = min((nh + C::HALF - 1) / kGroup, NB - 1);
+      const float* sw0 = a.sw + static_cast<size_t>(b0) * G;
+      const float* sw1 = a.sw + static_cast<size_t>(b1) * G;
+      const int cross = (b0 + 1) * kGroup - nh;  // first column of the second block
+      uint64_t acc[C::HALF / 2];
+#pragma unroll
+      for (int i = 0; i < C::HALF / 2; ++i) acc[i] = 0ull;
+      constexpr int PF = 4;  // groups whose scales are fetched ahead
+      float sx[PF], w0[PF], w1[PF];
+      auto fetch = [&](int g, float& x, float& u, float& v) {
+        const int gc = min(g, G - 1);
+        x = __ldg(sxp + static_cast<size_t>(gc) * a.lds);
+        u = __ldg(sw0 + gc);
+        if constexpr (BN % 256 != 0) v = __ldg(sw1 + gc);
+      };
+#pragma unroll
+      for (int j = 0; j < PF; ++j) fetch(j, sx[j], w0[j], w1[j]);
+      for (int g0 = 0; g0 < G && alive; g0 += PF) {
+#pragma unroll
+        for (int j = 0; j < PF; ++j) {
+          if (g0 + j < G && alive) {
+            const uint32_t buf = it & 1u;
+            const float x = sx[j];
+            const uint64_t s0 = twice(__fmul_rn(x, w0[j]));
+            const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, w1[j])) : s0;
+            fetch(g0 + j + PF, sx[j], w0[j], w1[j]);
+            alive = __all_sync(0xffffffffu, mbar_wait(&tfull[buf], (it >> 1) & 1u, tmo, abort_flag));
+            if (alive) {
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < CH; ++c) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(t_row + buf * 256u + static_cast<uint32_t>(c * 32), r);
+                tmem_wait_ld();
+                if (c == CH - 1) {  // the buffer is read: hand it back to the leader
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8u);
+                }
+                const uint64_t s = (BN % 256 != 0 && c * 32 >= cross) ? s1 : s0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], r[2 * i], r[2 * i + 1], s);
+              }
+              ++it;
+            }
+          }
+        }
+      }
+      if (!alive) {
+        if (lane == 0) gfail(a, abort_flag);
+        break;
+      }
+      if (row_ok) {
+        TY* yp = static_cast<TY*>(a.Y) + static_cast<size_t>(m) * N + nh;
+        const TY* bp = static_cast<const TY*>(a.bias) + nh;
+        const bool y32 = (reinterpret_cast<uintptr_t>(a.Y) & 31u) == 0;
+#pragma unroll
+        for (int c = 0; c < C::HALF / 16; ++c) {  // 16 columns at a time; N is a multiple of 16
+          if (nh + c * 16 < N) {
+            uint4 o[2];
+            uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+            uint4 b[2] = {};
+            if (a.bias != nullptr) {
+              b[0] = __ldg(reinterpret_cast<const uint4*>(bp + c * 16));
+              b[1] = __ldg(reinterpret_cast<const uint4*>(bp + c * 16) + 1);
+            }
+            const uint32_t* bw = reinterpret_cast<const uint32_t*>(b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float2 v = halves(acc[c * 8 + i]);
+              if (a.bias != nullptr) {
+                const float2 bb = pair_to_float<TY>(bw[i]);
+                v.x = __fadd_rn(v.x, bb.x);
+                v.y = __fadd_rn(v.y, bb.y);
+              }
+              ow[i] = float_to_pair<TY>(v.x, v.y);
+            }
+            uint4* d = reinterpret_cast<uint4*>(yp + c * 16);
+            if (y32) {
+              st_global_256(d, o[0], o[1]);
+            } else {
+              d[0] = o[0];
+              d[1] = o[1];
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+template <int BN, typename TY>
+cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const BlockGemmArgs& a, int num_sms,
+                        cudaStream_t stream) {
+  auto kern = block_gemm_pair_kernel<BN, TY>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<BN>::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((a.M + TILE_M - 1) / TILE_M) * ((a.N + BN - 1) / BN);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, num_sms / 2) * 2));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = PCfg<BN>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tmX, tmW, a);
 }
 
 }  // namespace
 
-cudaError_t launch_block_gemm(const BlockGemmArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  const dim3 grid((a.N + T - 1) / T, (a.M + T - 1) / T);
-  if (a.bf16) block_gemm_simple_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-  else block_gemm_simple_kernel<__half><<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+// Time of the fullest pair in columns of 256 rows: rounds of tiles x (width
+// + a fixed cost per tile).
+int block_pair_width(int64_t M, int64_t N, int num_sms) {
+  const int64_t pairs = std::max(1, num_sms / 2), num_m = (M + TILE_M - 1) / TILE_M;
+  int best = 0;
+  int64_t best_cost = 0;
+  for (int w : kPairWidths) {
+    const int64_t rounds = (num_m * ((N + w - 1) / w) + pairs - 1) / pairs;
+    const int64_t cost = rounds * (w + 8);
+    if (best == 0 || cost < best_cost) {
+      best = w;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const BlockGemmArgs& a, int width,
+                                   int num_sms, cudaStream_t stream) {
+#define PAIR(W)                                                                    \
+  if (width == W)                                                                  \
+    return a.bf16 ? launch_pair<W, __nv_bfloat16>(tmX, tmW, a, num_sms, stream)    \
+                  : launch_pair<W, __half>(tmX, tmW, a, num_sms, stream)
+  PAIR(256);
+  PAIR(192);
+  PAIR(128);
+#undef PAIR
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace i8mm

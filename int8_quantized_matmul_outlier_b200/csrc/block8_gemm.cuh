@@ -3,5 +3,12 @@
 #include "block8.cuh"
 
 namespace i8mm {
-cudaError_t launch_block_gemm(const BlockGemmArgs& a, int num_sms, cudaStream_t stream);
+
+// Columns of a tile of the CTA-pair kernel (rows: 256).
+constexpr int kPairWidths[] = {256, 192, 128};
+int block_pair_width(int64_t M, int64_t N, int num_sms);
+// tmX maps the codes [M, K] with 128-row boxes, tmW the weight's rows of 128
+// bytes with width / 2-row boxes.
+cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const BlockGemmArgs& a, int width,
+                                   int num_sms, cudaStream_t stream);
 }  // namespace i8mm
