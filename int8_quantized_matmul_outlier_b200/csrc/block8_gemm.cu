@@ -14,17 +14,21 @@
 // leader's barrier), keeps its 128 rows of P_g in its own TMEM, sums and
 // writes them.  No multicast.
 //   warp 0      TMA producer
-//   warp 1      allocates TMEM; in the leader one thread issues 4 MMAs of
-//               256 x BN x 32 per group, alternating between two buffers
-//   warps 4-11  two per TMEM lane quarter, one row per thread and half of the
-//               tile's columns: they add P_g times sx sw to BN / 2 registers
-//               and write Y at the tile's end, while the next tile's first
-//               two groups already run
-// A group takes the tensor cores 2 BN cycles (BN = 256: 512); in that time
-// the eight warps read 128 x BN values (256 cycles of TMEM reads) and make as
-// many multiply-adds (256 cycles, two per packed instruction), so the sums
-// hide behind the tensor cores as long as a buffer is handed back within one
-// group's time.
+//   warp 1      allocates TMEM; in the leader one lane issues the MMAs, a group
+//               in two units of half the tile's columns (4 MMAs of 256 x
+//               BN / 2 x 32 each), round-robin over four TMEM slots
+//   warps 4-11  two per TMEM lane quarter, one row per thread and half of
+//               every unit's columns: they add P_g times sx sw to BN / 2
+//               registers and write Y at the tile's end, while the next
+//               tile's first two groups already run
+// A unit takes the tensor cores BN cycles (BN = 256: 256).  From its issue to
+// its slot's next use pass its own time, the commit (about 190 cycles), the
+// reads (200), the arrivals at the leader (200) and the issue (100): under
+// four units' time, but not under two groups' time of 512-column buffers,
+// whose reads take 400 (whole groups in two buffers ran at 990 cycles per
+// group).  The reads of the next 32 columns run under the multiply-adds of the
+// last; the eight warps' multiply-adds need 262 cycles per group of 512
+// (measured alone, two per packed instruction).
 //
 // BN: the tile width is chosen from 256, 192 and 128 so that the tiles fill
 // the pairs' rounds (block_pair_width).  A 192-wide tile does not start on a
@@ -54,21 +58,36 @@ constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int REGS_LAUNCH = 168, REGS_FRONT = 72, REGS_EPI = 216;
 static_assert(128 * REGS_FRONT + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS_LAUNCH, "registers within the launch's");
 
+// TMEM: four slots of 128 columns.
+constexpr int SLOTS = 4, SLOT_COLS = 128;
+
+// Scales of a CTA's rows, one group per ring slot.  The producer fills slot g
+// % 16 once stage g - STAGES is free, i.e. once the MMAs of group g - STAGES
+// are done; those were issued after both CTAs' epilogues had handed back
+// group g - STAGES - 2, which they do after reading its scales: the slot's
+// last reader, of group g - 16, is done as long as STAGES + 2 <= 16.
+constexpr int SX_RING = 16;
+
 template <int BN>
 struct PCfg {
   static constexpr int A_BYTES = BM * kGroup;
   static constexpr int B_BYTES = BN / 2 * kGroup;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 229376 / STAGE;
+  static constexpr int STAGES = 212992 / STAGE;
   static constexpr int HALF = BN / 2;  // columns per epilogue warp
-  static constexpr int NBARS = 2 * STAGES + 5;
-  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int UNIT = BN / 2;  // columns of a unit, half from each CTA's rows of W
+  static constexpr int WCOLS = UNIT / 2;  // a warp's columns of a unit
+  static constexpr int NBARS = 2 * STAGES + 2 * SLOTS + 1 + SX_RING;
+  static constexpr int SX_OFF = STAGES * STAGE;
+  static constexpr int BAR_OFF = SX_OFF + SX_RING * BM * 4;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;  // + slack to align the base to 1024
-  static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, BN);  // e4m3 and fp16 operands share the encoding 0
-  static_assert(HALF % 32 == 0 && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
+  static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, UNIT);  // e4m3 and fp16 operands share the encoding 0
+  static_assert(STAGES + 2 <= SX_RING, "");
+  static_assert(UNIT % 32 == 0 && UNIT <= SLOT_COLS && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
 };
 
+// D[tmem of both CTAs] (+)= A * B^T over the pair's shared memory, e4m3 to fp32.
 __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                               uint32_t accumulate) {
   asm volatile(
@@ -77,6 +96,24 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, u
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// 1 in one lane of the (converged) warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// Untiled copy of `bytes` (a multiple of 16) to shared memory, counted on
+// this CTA's barrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ uint64_t make_desc(uint32_t lo, uint32_t hi) {
+  return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
 __device__ __forceinline__ void gfail(const BlockGemmArgs& a, volatile int* abort_flag) {
@@ -110,6 +147,30 @@ __device__ __forceinline__ float2 halves(uint64_t v) {
   return f;
 }
 
+// N consecutive columns of this thread's TMEM lane (N = 16 or 32).
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) tmem_ld_32x32b_x32(taddr, r);
+  else tmem_ld_32x32b_x16(taddr, r);
+  static_assert(N == 16 || N == 32, "");
+}
+
+// Waits for this thread's TMEM reads.  The registers they fill go through the
+// statement, so that no use of them can move above it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[N]) {
+  if constexpr (N == 32)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+  else
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 template <int BN, typename TY>
 __global__ void __launch_bounds__(THREADS, 1)
     block_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -120,12 +181,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + SLOTS;
+  uint64_t* drain = tempty + SLOTS;
+  uint64_t* sfull = drain + 1;
+  float* sx_s = reinterpret_cast<float*>(smem + C::SX_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int M = a.M, N = a.N;
   const uint32_t rank = cluster_ctarank();
   const int tile0 = static_cast<int>(blockIdx.x) / 2;
@@ -139,11 +202,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < SLOTS; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], EPI_WARPS * 2);
     }
     mbar_init(drain, 1);
+    for (int s = 0; s < SX_RING; ++s) mbar_init(&sfull[s], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmX);
@@ -165,13 +229,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
       int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_phase = 0, it = 0;
       bool ok = true;
       const uint64_t pol_x = l2_policy_evict_last();  // every column tile of its rows reads X again
       for (int t = tile0; t < num_tiles && ok; t += tstride) {
         const int m0 = (t % num_m) * TILE_M + static_cast<int>(rank) * BM;
         const int n0 = (t / num_m) * BN + static_cast<int>(rank) * (BN / 2);
-        for (int g = 0; g < G; ++g) {
+        // rows of scales: up to lds, a multiple of 4 (16 bytes)
+        const uint32_t sx_bytes = static_cast<uint32_t>(max(0, min(BM, (M - m0 + 3) & ~3))) * 4u;
+        for (int g = 0; g < G; ++g, ++it) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, tmo, abort_flag)) {
             ok = false;
             break;
@@ -183,6 +249,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* st = smem + stage * C::STAGE;
           tma_load_2d_pair_hint(st, &tmX, bar, g * kGroup, m0, pol_x);
           tma_load_2d_pair(st + C::A_BYTES, &tmW, bar, 0, g * a.N_pad + n0);
+          uint64_t* sb = &sfull[it % SX_RING];
+          if (sx_bytes != 0u) {
+            mbar_arrive_expect_tx(sb, sx_bytes);
+            bulk_load(sx_s + (it % SX_RING) * BM, a.sx + static_cast<size_t>(g) * a.lds + m0, sx_bytes, sb);
+          } else {
+            mbar_arrive(sb);
+          }
           issued_mask |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == C::STAGES) {
@@ -193,6 +266,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!ok) {
         gfail(a, abort_flag);
+        for (uint32_t j = it > SX_RING ? it - SX_RING : 0; j < it; ++j)
+          mbar_wait(&sfull[j % SX_RING], (j / SX_RING) & 1u, tmo, nullptr);
         // every load already issued lands before the CTA can exit (the peer
         // cannot watch the leader's barriers: it waits a while)
         if (rank == 0) {
@@ -206,36 +281,45 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
    } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // -------------------------------------------------------- MMA issuer
+      // The whole warp walks the loop and one elected lane issues: the
+      // descriptors then stay in uniform registers.
+      const uint32_t issuer = elect_one();
+      const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_k_sw128(0) >> 32);
+      const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_k_sw128(smem_u32(smem)));
       int stage = 0;
       uint32_t phase = 0, it = 0;
       bool ok = true;
       for (int t = tile0; t < num_tiles && ok; t += tstride) {
-        for (int g = 0; g < G; ++g, ++it) {
-          const uint32_t buf = it & 1u;
-          if (!mbar_wait(&tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag) ||
-              !mbar_wait(&full[stage], phase, tmo, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * C::STAGE);
-          const uint64_t adesc = smem_desc_k_sw128(sa);
-          const uint64_t bdesc = smem_desc_k_sw128(sa + C::A_BYTES);
+        for (int g = 0; g < G && ok; ++g, ++it) {
+          ok = mbar_wait_warp(&full[stage], phase, tmo, abort_flag);
 #pragma unroll
-          for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
-            mma_e4m3_pair(tmem_base + buf * 256u, adesc + static_cast<uint64_t>(kk * 2),
-                          bdesc + static_cast<uint64_t>(kk * 2), C::IDESC, kk != 0 ? 1u : 0u);
-          mma_commit_pair(&tfull[buf], 0x3);
-          mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
+          for (int u = 0; u < 2 && ok; ++u) {
+            const uint32_t slot = (it & 1u) * 2u + u;
+            ok = mbar_wait_warp(&tempty[slot], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag);
+            if (ok) {
+              tc_fence_after();
+              if (issuer) {
+                const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
+                const uint32_t bd = ad + ((C::A_BYTES + u * C::WCOLS * kGroup) >> 4);
+                const uint32_t d = tmem_base + slot * SLOT_COLS;
+#pragma unroll
+                for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
+                  mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
+                mma_commit_pair(&tfull[slot], 0x3);
+                if (u == 1) mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
+              }
+              __syncwarp();
+            }
+          }
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (!ok) {
+      if (!ok && issuer) {
         gfail(a, abort_flag);
         mma_commit_pair(drain, 0x1);
         mbar_wait(drain, 0, tmo, nullptr);
@@ -247,9 +331,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ----------------------------------------------------- sums and epilogue
     const int q = warp & 3;             // TMEM lane quarter this warp may read
     const int h = (warp - 4) >> 2;      // half of the tile's columns
-    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
+    // a unit's columns from this CTA pair's rows of W: those of rank h are the
+    // unit's half h, so this warp's columns of the two units are neighbours in Y
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::WCOLS);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
-    constexpr int CH = C::HALF / 32;
     const int NB = (N + kGroup - 1) / kGroup;
     uint32_t it = 0;
     bool alive = true;
@@ -257,56 +342,67 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int m = (t % num_m) * TILE_M + static_cast<int>(rank) * BM + q * 32 + lane;
       const int nh = (t / num_m) * BN + h * C::HALF;
       const bool row_ok = m < M;
-      // the scales: this row's, and those of the one or two weight blocks
-      // that the half-tile meets (past N: any block's, the sums are dropped)
-      const float* sxp = a.sx + (row_ok ? m : 0);
+      // the weight scales of the one or two blocks that the half-tile meets
+      // (past N: any block's, the sums are dropped), 32 groups at a time, one
+      // per lane
       const int b0 = min(nh / kGroup, NB - 1), b1 = min((nh + C::HALF - 1) / kGroup, NB - 1);
       const float* sw0 = a.sw + static_cast<size_t>(b0) * G;
       const float* sw1 = a.sw + static_cast<size_t>(b1) * G;
+      float w0 = 0.0f, w1 = 0.0f;
       const int cross = (b0 + 1) * kGroup - nh;  // first column of the second block
       uint64_t acc[C::HALF / 2];
 #pragma unroll
       for (int i = 0; i < C::HALF / 2; ++i) acc[i] = 0ull;
-      constexpr int PF = 4;  // groups whose scales are fetched ahead
-      float sx[PF], w0[PF], w1[PF];
-      auto fetch = [&](int g, float& x, float& u, float& v) {
-        const int gc = min(g, G - 1);
-        x = __ldg(sxp + static_cast<size_t>(gc) * a.lds);
-        u = __ldg(sw0 + gc);
-        if constexpr (BN % 256 != 0) v = __ldg(sw1 + gc);
+      auto unit_ready = [&](uint32_t i, int u) {
+        alive = mbar_wait_warp(&tfull[(i & 1u) * 2u + u], (i >> 1) & 1u, tmo, abort_flag);
+        tc_fence_after();
+        return alive;
       };
+      auto unit_addr = [&](uint32_t i, int u) { return t_row + ((i & 1u) * 2u + u) * SLOT_COLS; };
+      auto hand_back = [&](uint32_t i, int u) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + ((i & 1u) * 2u + u) * 8u);
+      };
+      // columns [c0, c0 + n) of the warp's half-tile += r times the scale
+      auto add = [&](const uint32_t* r, int c0, int n, uint64_t s0, uint64_t s1) {
 #pragma unroll
-      for (int j = 0; j < PF; ++j) fetch(j, sx[j], w0[j], w1[j]);
-      for (int g0 = 0; g0 < G && alive; g0 += PF) {
-#pragma unroll
-        for (int j = 0; j < PF; ++j) {
-          if (g0 + j < G && alive) {
-            const uint32_t buf = it & 1u;
-            const float x = sx[j];
-            const uint64_t s0 = twice(__fmul_rn(x, w0[j]));
-            const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, w1[j])) : s0;
-            fetch(g0 + j + PF, sx[j], w0[j], w1[j]);
-            alive = __all_sync(0xffffffffu, mbar_wait(&tfull[buf], (it >> 1) & 1u, tmo, abort_flag));
-            if (alive) {
-              tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < CH; ++c) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(t_row + buf * 256u + static_cast<uint32_t>(c * 32), r);
-                tmem_wait_ld();
-                if (c == CH - 1) {  // the buffer is read: hand it back to the leader
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
-                }
-                const uint64_t s = (BN % 256 != 0 && c * 32 >= cross) ? s1 : s0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], r[2 * i], r[2 * i + 1], s);
-              }
-              ++it;
-            }
+        for (int i = 0; i < n / 2; ++i)
+          fma2(acc[c0 / 2 + i], r[2 * i], r[2 * i + 1], (BN % 256 != 0 && c0 + (2 * i & ~15) >= cross) ? s1 : s0);
+      };
+      constexpr int C0 = C::WCOLS > 32 ? 32 : C::WCOLS / 2, C1 = C::WCOLS - C0;  // a unit's two reads
+      uint32_t ra[C0], rb[C1];
+      if (unit_ready(it, 0)) {
+        tmem_ld_cols<C0>(unit_addr(it, 0), ra);
+#pragma unroll 1
+        for (int g = 0; g < G; ++g, ++it) {
+          if ((g & 31) == 0) {
+            w0 = __ldg(sw0 + min(g + lane, G - 1));
+            if constexpr (BN % 256 != 0) w1 = __ldg(sw1 + min(g + lane, G - 1));
           }
+          // (read through shared memory: with the row's scale loaded from
+          // global memory here, groups ahead of its use, the next
+          // tcgen05.wait::ld waited for that load too)
+          alive = mbar_wait_warp(&sfull[it % SX_RING], (it / SX_RING) & 1u, tmo, abort_flag);
+          if (!alive) break;
+          const float x = sx_s[(it % SX_RING) * BM + q * 32 + lane];
+          const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, g & 31)));
+          const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, g & 31))) : s0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            tmem_wait_cols(ra);
+            tmem_ld_cols<C1>(unit_addr(it, u) + C0, rb);
+            add(ra, u * C::WCOLS, C0, s0, s1);
+            tmem_wait_cols(rb);
+            hand_back(it, u);
+            const uint32_t ni = it + u;
+            if ((u == 0 || g + 1 < G) && unit_ready(ni, u ^ 1)) tmem_ld_cols<C0>(unit_addr(ni, u ^ 1), ra);
+            if (!alive) break;
+            add(rb, u * C::WCOLS + C0, C1, s0, s1);
+          }
+          if (!alive) break;
         }
+        tmem_wait_ld();
       }
       if (!alive) {
         if (lane == 0) gfail(a, abort_flag);

@@ -65,6 +65,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The same for a converged warp, all lanes together, where buffers go to and
+// fro between warps within a few hundred cycles: polls without suspending.  A
+// try_wait that finds its phase open comes back after about 150 cycles, so a
+// chain of three such waits costs several hundred more than the work between
+// them.  After 4096 polls it waits as mbar_wait does.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                               volatile int* abort) {
+#pragma unroll 1
+  for (int i = 0; i < 4096; ++i)
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, timeout_ns, abort));
+}
+
 // Load with acquire semantics at GPU scope (a flag another CTA releases).
 __device__ __forceinline__ uint32_t ld_acquire_gpu_u32(const uint32_t* p) {
   uint32_t v;
