@@ -14,21 +14,22 @@
 // leader's barrier), keeps its 128 rows of P_g in its own TMEM, sums and
 // writes them.  No multicast.
 //   warp 0      TMA producer
-//   warp 1      allocates TMEM; in the leader one lane issues the MMAs, a group
-//               in two units of half the tile's columns (4 MMAs of 256 x
-//               BN / 2 x 32 each), round-robin over four TMEM slots
-//   warps 4-11  two per TMEM lane quarter, one row per thread and half of
-//               every unit's columns: they add P_g times sx sw to BN / 2
-//               registers and write Y at the tile's end, while the next
-//               tile's first two groups already run
-// A unit takes the tensor cores BN cycles (BN = 256: 256).  From its issue to
-// its slot's next use pass its own time, the commit (about 190 cycles), the
-// reads (200), the arrivals at the leader (200) and the issue (100): under
-// four units' time, but not under two groups' time of 512-column buffers,
-// whose reads take 400 (whole groups in two buffers ran at 990 cycles per
-// group).  The reads of the next 32 columns run under the multiply-adds of the
-// last; the eight warps' multiply-adds need 262 cycles per group of 512
-// (measured alone, two per packed instruction).
+//   warp 1      allocates TMEM; in the leader one lane issues the MMAs of a
+//               group (4 of 256 x BN x 32), alternating between two buffers
+//   warps 4-11  two per TMEM lane quarter, one row per thread and half of the
+//               tile's columns: they add P_g times sx sw to BN / 2 registers
+//               and write Y at the tile's end, while the next tile's first
+//               two groups already run
+// A group takes the tensor cores 2 BN cycles (BN = 256: 512).  Reading 128 x
+// 256 values from TMEM takes the eight warps 142 cycles, adding them 262 (two
+// per packed instruction), both measured alone, so the sums fit beside the
+// tensor cores; what bounds the kernel is the way of a buffer: its MMAs, the
+// commit, the reads, the arrivals at the leader, the next issue.  A barrier
+// poll takes 200 cycles and more while the MMAs read shared memory, so waits
+// are polled ahead or two at a time, and the reads of the next 32 columns run
+// under the multiply-adds of the last.
+// Units of half a group (N = 128, four buffers) would have more slack, but
+// read the X tile twice from shared memory: 1393 us for 2048 x 12288 x 49152.
 //
 // BN: the tile width is chosen from 256, 192 and 128 so that the tiles fill
 // the pairs' rounds (block_pair_width).  A 192-wide tile does not start on a
@@ -58,8 +59,8 @@ constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int REGS_LAUNCH = 168, REGS_FRONT = 72, REGS_EPI = 216;
 static_assert(128 * REGS_FRONT + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS_LAUNCH, "registers within the launch's");
 
-// TMEM: four slots of 128 columns.
-constexpr int SLOTS = 4, SLOT_COLS = 128;
+// TMEM: two buffers of 256 columns.
+constexpr int SLOTS = 2, SLOT_COLS = 256;
 
 // Scales of a CTA's rows, one group per ring slot.  The producer fills slot g
 // % 16 once stage g - STAGES is free, i.e. once the MMAs of group g - STAGES
@@ -75,16 +76,14 @@ struct PCfg {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 212992 / STAGE;
   static constexpr int HALF = BN / 2;  // columns per epilogue warp
-  static constexpr int UNIT = BN / 2;  // columns of a unit, half from each CTA's rows of W
-  static constexpr int WCOLS = UNIT / 2;  // a warp's columns of a unit
   static constexpr int NBARS = 2 * STAGES + 2 * SLOTS + 1 + SX_RING;
   static constexpr int SX_OFF = STAGES * STAGE;
   static constexpr int BAR_OFF = SX_OFF + SX_RING * BM * 4;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;  // + slack to align the base to 1024
-  static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, UNIT);  // e4m3 and fp16 operands share the encoding 0
+  static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, BN);  // e4m3 and fp16 operands share the encoding 0
   static_assert(STAGES + 2 <= SX_RING, "");
-  static_assert(UNIT % 32 == 0 && UNIT <= SLOT_COLS && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
+  static_assert(HALF % 32 == 0 && BN <= SLOT_COLS && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
 };
 
 // D[tmem of both CTAs] (+)= A * B^T over the pair's shared memory, e4m3 to fp32.
@@ -147,28 +146,13 @@ __device__ __forceinline__ float2 halves(uint64_t v) {
   return f;
 }
 
-// N consecutive columns of this thread's TMEM lane (N = 16 or 32).
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 32) tmem_ld_32x32b_x32(taddr, r);
-  else tmem_ld_32x32b_x16(taddr, r);
-  static_assert(N == 16 || N == 32, "");
-}
-
 // Waits for this thread's TMEM reads.  The registers they fill go through the
 // statement, so that no use of them can move above it.
-template <int N>
-__device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[N]) {
-  if constexpr (N == 32)
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-  else
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+__device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 template <int BN, typename TY>
@@ -293,25 +277,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int t = tile0; t < num_tiles && ok; t += tstride) {
         for (int g = 0; g < G && ok; ++g, ++it) {
-          ok = mbar_wait_warp(&full[stage], phase, tmo, abort_flag);
+          const uint32_t buf = it & 1u;
+          ok = mbar_wait2_warp(&full[stage], phase, &tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag);
+          if (ok) {
+            tc_fence_after();
+            if (issuer) {
+              const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
+              const uint32_t bd = ad + (C::A_BYTES >> 4);
+              const uint32_t d = tmem_base + buf * SLOT_COLS;
 #pragma unroll
-          for (int u = 0; u < 2 && ok; ++u) {
-            const uint32_t slot = (it & 1u) * 2u + u;
-            ok = mbar_wait_warp(&tempty[slot], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag);
-            if (ok) {
-              tc_fence_after();
-              if (issuer) {
-                const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
-                const uint32_t bd = ad + ((C::A_BYTES + u * C::WCOLS * kGroup) >> 4);
-                const uint32_t d = tmem_base + slot * SLOT_COLS;
-#pragma unroll
-                for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
-                  mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
-                mma_commit_pair(&tfull[slot], 0x3);
-                if (u == 1) mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
-              }
-              __syncwarp();
+              for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
+                mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
+              mma_commit_pair(&tfull[buf], 0x3);
+              mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
             }
+            __syncwarp();
           }
           if (++stage == C::STAGES) {
             stage = 0;
@@ -331,10 +311,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ----------------------------------------------------- sums and epilogue
     const int q = warp & 3;             // TMEM lane quarter this warp may read
     const int h = (warp - 4) >> 2;      // half of the tile's columns
-    // a unit's columns from this CTA pair's rows of W: those of rank h are the
-    // unit's half h, so this warp's columns of the two units are neighbours in Y
-    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::WCOLS);
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    constexpr int CH = C::HALF / 32;
     const int NB = (N + kGroup - 1) / kGroup;
     uint32_t it = 0;
     bool alive = true;
@@ -353,56 +332,57 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint64_t acc[C::HALF / 2];
 #pragma unroll
       for (int i = 0; i < C::HALF / 2; ++i) acc[i] = 0ull;
-      auto unit_ready = [&](uint32_t i, int u) {
-        alive = mbar_wait_warp(&tfull[(i & 1u) * 2u + u], (i >> 1) & 1u, tmo, abort_flag);
-        tc_fence_after();
-        return alive;
-      };
-      auto unit_addr = [&](uint32_t i, int u) { return t_row + ((i & 1u) * 2u + u) * SLOT_COLS; };
-      auto hand_back = [&](uint32_t i, int u) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + ((i & 1u) * 2u + u) * 8u);
-      };
-      // columns [c0, c0 + n) of the warp's half-tile += r times the scale
-      auto add = [&](const uint32_t* r, int c0, int n, uint64_t s0, uint64_t s1) {
+      // columns [32 c, 32 c + 32) of the warp's half-tile += r times the scale
+      auto add = [&](const uint32_t (&r)[32], int c, uint64_t s0, uint64_t s1) {
 #pragma unroll
-        for (int i = 0; i < n / 2; ++i)
-          fma2(acc[c0 / 2 + i], r[2 * i], r[2 * i + 1], (BN % 256 != 0 && c0 + (2 * i & ~15) >= cross) ? s1 : s0);
+        for (int i = 0; i < 16; ++i)
+          fma2(acc[c * 16 + i], r[2 * i], r[2 * i + 1], (BN % 256 != 0 && c * 32 >= cross) ? s1 : s0);
       };
-      constexpr int C0 = C::WCOLS > 32 ? 32 : C::WCOLS / 2, C1 = C::WCOLS - C0;  // a unit's two reads
-      uint32_t ra[C0], rb[C1];
-      if (unit_ready(it, 0)) {
-        tmem_ld_cols<C0>(unit_addr(it, 0), ra);
+      // (the row's scales come through shared memory: with the next ones on
+      // their way from global memory, tcgen05.wait::ld waited for them too)
+      const float* sxl = sx_s + q * 32 + lane;
+      bool ready = false;  // this group's barriers were complete when polled during the last one
+      float x = 0.0f;
 #pragma unroll 1
-        for (int g = 0; g < G; ++g, ++it) {
-          if ((g & 31) == 0) {
-            w0 = __ldg(sw0 + min(g + lane, G - 1));
-            if constexpr (BN % 256 != 0) w1 = __ldg(sw1 + min(g + lane, G - 1));
-          }
-          // (read through shared memory: with the row's scale loaded from
-          // global memory here, groups ahead of its use, the next
-          // tcgen05.wait::ld waited for that load too)
-          alive = mbar_wait_warp(&sfull[it % SX_RING], (it / SX_RING) & 1u, tmo, abort_flag);
-          if (!alive) break;
-          const float x = sx_s[(it % SX_RING) * BM + q * 32 + lane];
-          const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, g & 31)));
-          const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, g & 31))) : s0;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            tmem_wait_cols(ra);
-            tmem_ld_cols<C1>(unit_addr(it, u) + C0, rb);
-            add(ra, u * C::WCOLS, C0, s0, s1);
-            tmem_wait_cols(rb);
-            hand_back(it, u);
-            const uint32_t ni = it + u;
-            if ((u == 0 || g + 1 < G) && unit_ready(ni, u ^ 1)) tmem_ld_cols<C0>(unit_addr(ni, u ^ 1), ra);
-            if (!alive) break;
-            add(rb, u * C::WCOLS + C0, C1, s0, s1);
-          }
-          if (!alive) break;
+      for (int g = 0; g < G; ++g, ++it) {
+        const uint32_t buf = it & 1u;
+        if ((g & 31) == 0) {
+          w0 = __ldg(sw0 + min(g + lane, G - 1));
+          if constexpr (BN % 256 != 0) w1 = __ldg(sw1 + min(g + lane, G - 1));
         }
-        tmem_wait_ld();
+        if (!__all_sync(0xffffffffu, ready)) {
+          alive = mbar_wait2_warp(&tfull[buf], (it >> 1) & 1u, &sfull[it % SX_RING], (it / SX_RING) & 1u, tmo,
+                                  abort_flag);
+          if (!alive) break;
+          x = sxl[(it % SX_RING) * BM];
+        }
+        tc_fence_after();
+        const uint32_t t = t_row + buf * SLOT_COLS;
+        uint32_t ra[32], rb[32];
+        tmem_ld_32x32b_x32(t, ra);
+        const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, g & 31)));
+        const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, g & 31))) : s0;
+        ready = false;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          uint32_t(&r)[32] = (c & 1) ? rb : ra;
+          uint32_t(&n)[32] = (c & 1) ? ra : rb;
+          tmem_wait_cols(r);
+          if (c + 1 < CH) {
+            tmem_ld_32x32b_x32(t + static_cast<uint32_t>((c + 1) * 32), n);
+          } else {  // the buffer is read: hand it back to the leader
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
+            if (g + 1 < G) {  // look ahead while the last columns are added
+              const uint32_t j = it + 1;
+              ready = mbar_test_wait(&tfull[j & 1u], (j >> 1) & 1u) &
+                      mbar_test_wait(&sfull[j % SX_RING], (j / SX_RING) & 1u);
+              x = sxl[(j % SX_RING) * BM];
+            }
+          }
+          add(r, c, s0, s1);
+        }
       }
       if (!alive) {
         if (lane == 0) gfail(a, abort_flag);

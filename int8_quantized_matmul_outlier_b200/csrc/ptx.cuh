@@ -77,17 +77,20 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same for a converged warp, all lanes together, where buffers go to and
-// fro between warps within a few hundred cycles: polls without suspending.  A
-// try_wait that finds its phase open comes back after about 150 cycles, so a
-// chain of three such waits costs several hundred more than the work between
-// them.  After 4096 polls it waits as mbar_wait does.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
-                                               volatile int* abort) {
+// mbar_wait for two barriers and a converged warp, all lanes together, where
+// buffers go to and fro between warps within a few hundred cycles: polls both
+// at a time and without suspending.  A try_wait that finds its phase open
+// comes back after about 150 cycles, so a chain of such waits costs more than
+// the work between them.  After 4096 polls it waits as mbar_wait does.
+__device__ __forceinline__ bool mbar_wait2_warp(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
+                                                uint64_t timeout_ns, volatile int* abort) {
 #pragma unroll 1
-  for (int i = 0; i < 4096; ++i)
-    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, timeout_ns, abort));
+  for (int i = 0; i < 4096; ++i) {
+    const bool a = mbar_test_wait(bar0, parity0), b = mbar_test_wait(bar1, parity1);
+    if (__all_sync(0xffffffffu, a & b)) return true;
+  }
+  return __all_sync(0xffffffffu,
+                    mbar_wait(bar0, parity0, timeout_ns, abort) && mbar_wait(bar1, parity1, timeout_ns, abort));
 }
 
 // Load with acquire semantics at GPU scope (a flag another CTA releases).
