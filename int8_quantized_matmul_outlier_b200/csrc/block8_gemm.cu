@@ -53,10 +53,10 @@ constexpr int BM = 128;  // rows per CTA
 constexpr int EPI_WARPS = 8;
 // Three warpgroups, so that registers can move between them: launched with
 // 168 each (384 x 168 = 64512), the first (producer, MMA issuer, two idle
-// warps) goes down to 72 and the two epilogue groups up to 216
-// (128 x 72 + 256 x 216 = 64512).
+// warps) goes down to 40 and the two epilogue groups up to 232
+// (128 x 40 + 256 x 232 = 64512).
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
-constexpr int REGS_LAUNCH = 168, REGS_FRONT = 72, REGS_EPI = 216;
+constexpr int REGS_LAUNCH = 168, REGS_FRONT = 40, REGS_EPI = 232;
 static_assert(128 * REGS_FRONT + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS_LAUNCH, "registers within the launch's");
 
 // TMEM: two buffers of 256 columns.
