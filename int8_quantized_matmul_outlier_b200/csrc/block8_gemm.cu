@@ -62,27 +62,23 @@ static_assert(128 * REGS_FRONT + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS_LAU
 // TMEM: two buffers of 256 columns.
 constexpr int SLOTS = 2, SLOT_COLS = 256;
 
-// Scales of a CTA's rows, one group per ring slot.  The producer fills slot g
-// % 16 once stage g - STAGES is free, i.e. once the MMAs of group g - STAGES
-// are done; those were issued after both CTAs' epilogues had handed back
-// group g - STAGES - 2, which they do after reading its scales: the slot's
-// last reader, of group g - 16, is done as long as STAGES + 2 <= 16.
-constexpr int SX_RING = 16;
+// Scales of a CTA's rows come up to SX_CHUNK groups of one tile at a time, two
+// chunks in turn.
+constexpr int SX_CHUNK = 16;
 
 template <int BN>
 struct PCfg {
   static constexpr int A_BYTES = BM * kGroup;
   static constexpr int B_BYTES = BN / 2 * kGroup;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 212992 / STAGE;
+  static constexpr int STAGES = 204800 / STAGE;
   static constexpr int HALF = BN / 2;  // columns per epilogue warp
-  static constexpr int NBARS = 2 * STAGES + 2 * SLOTS + 1 + SX_RING;
+  static constexpr int NBARS = 2 * STAGES + 2 * SLOTS + 1 + 4;
   static constexpr int SX_OFF = STAGES * STAGE;
-  static constexpr int BAR_OFF = SX_OFF + SX_RING * BM * 4;
+  static constexpr int BAR_OFF = SX_OFF + 2 * SX_CHUNK * BM * 4;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;  // + slack to align the base to 1024
   static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, BN);  // e4m3 and fp16 operands share the encoding 0
-  static_assert(STAGES + 2 <= SX_RING, "");
   static_assert(HALF % 32 == 0 && BN <= SLOT_COLS && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
 };
 
@@ -146,6 +142,12 @@ __device__ __forceinline__ float2 halves(uint64_t v) {
   return f;
 }
 
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // Waits for this thread's TMEM reads.  The registers they fill go through the
 // statement, so that no use of them can move above it.
 __device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[32]) {
@@ -168,6 +170,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* tempty = tfull + SLOTS;
   uint64_t* drain = tempty + SLOTS;
   uint64_t* sfull = drain + 1;
+  uint64_t* sempty = sfull + 2;
   float* sx_s = reinterpret_cast<float*>(smem + C::SX_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
@@ -180,6 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int num_m = (M + TILE_M - 1) / TILE_M;
   const int num_tiles = num_m * ((N + BN - 1) / BN);
   const int G = (a.K + kGroup - 1) / kGroup;
+  const int G2 = (G + 1) & ~1;  // groups are taken in pairs, one per TMEM buffer
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -191,7 +195,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&tempty[b], EPI_WARPS * 2);
     }
     mbar_init(drain, 1);
-    for (int s = 0; s < SX_RING; ++s) mbar_init(&sfull[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sempty[s], EPI_WARPS);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmX);
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
       int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_phase = 0, it = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_phase = 0, chunk = 0;
       bool ok = true;
       const uint64_t pol_x = l2_policy_evict_last();  // every column tile of its rows reads X again
       for (int t = tile0; t < num_tiles && ok; t += tstride) {
@@ -221,8 +228,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int n0 = (t / num_m) * BN + static_cast<int>(rank) * (BN / 2);
         // rows of scales: up to lds, a multiple of 4 (16 bytes)
         const uint32_t sx_bytes = static_cast<uint32_t>(max(0, min(BM, (M - m0 + 3) & ~3))) * 4u;
-        for (int g = 0; g < G; ++g, ++it) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, tmo, abort_flag)) {
+        for (int g = 0; g < G; ++g) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, tmo, abort_flag) ||
+              (g % SX_CHUNK == 0 && !mbar_wait(&sempty[chunk & 1u], ((chunk >> 1) & 1u) ^ 1u, tmo, abort_flag))) {
             ok = false;
             break;
           }
@@ -233,12 +241,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* st = smem + stage * C::STAGE;
           tma_load_2d_pair_hint(st, &tmX, bar, g * kGroup, m0, pol_x);
           tma_load_2d_pair(st + C::A_BYTES, &tmW, bar, 0, g * a.N_pad + n0);
-          uint64_t* sb = &sfull[it % SX_RING];
-          if (sx_bytes != 0u) {
-            mbar_arrive_expect_tx(sb, sx_bytes);
-            bulk_load(sx_s + (it % SX_RING) * BM, a.sx + static_cast<size_t>(g) * a.lds + m0, sx_bytes, sb);
-          } else {
-            mbar_arrive(sb);
+          if (g % SX_CHUNK == 0) {
+            uint64_t* sb = &sfull[chunk & 1u];
+            float* dst = sx_s + (chunk & 1u) * (SX_CHUNK * BM);
+            const int n = min(SX_CHUNK, G - g);
+            if (sx_bytes != 0u) {
+              mbar_arrive_expect_tx(sb, sx_bytes * static_cast<uint32_t>(n));
+              for (int j = 0; j < n; ++j)
+                bulk_load(dst + j * BM, a.sx + static_cast<size_t>(g + j) * a.lds + m0, sx_bytes, sb);
+            } else {
+              mbar_arrive(sb);
+            }
+            ++chunk;
           }
           issued_mask |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -250,8 +264,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!ok) {
         gfail(a, abort_flag);
-        for (uint32_t j = it > SX_RING ? it - SX_RING : 0; j < it; ++j)
-          mbar_wait(&sfull[j % SX_RING], (j / SX_RING) & 1u, tmo, nullptr);
+        for (uint32_t j = chunk > 2 ? chunk - 2 : 0; j < chunk; ++j)
+          mbar_wait(&sfull[j & 1u], (j >> 1) & 1u, tmo, nullptr);
         // every load already issued lands before the CTA can exit (the peer
         // cannot watch the leader's barriers: it waits a while)
         if (rank == 0) {
@@ -276,8 +290,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t phase = 0, it = 0;
       bool ok = true;
       for (int t = tile0; t < num_tiles && ok; t += tstride) {
-        for (int g = 0; g < G && ok; ++g, ++it) {
+        for (int g = 0; g < G2 && ok; ++g, ++it) {
           const uint32_t buf = it & 1u;
+          if (g == G) {  // an odd tile's last group is empty: no MMAs, only the commit
+            ok = mbar_wait2_warp(&tempty[buf], ((it >> 1) & 1u) ^ 1u, &tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo,
+                                 abort_flag);
+            if (ok && issuer) mma_commit_pair(&tfull[buf], 0x3);
+            __syncwarp();
+            continue;
+          }
           ok = mbar_wait2_warp(&full[stage], phase, &tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag);
           if (ok) {
             tc_fence_after();
@@ -315,19 +336,22 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     constexpr int CH = C::HALF / 32;
     const int NB = (N + kGroup - 1) / kGroup;
-    uint32_t it = 0;
+    uint32_t chunk = 0, ph = 0;
     bool alive = true;
+    const uint32_t tfull0 = smem_u32(&tfull[0]);
+    const uint32_t sx0 = smem_u32(sx_s) + static_cast<uint32_t>(q * 32 + lane) * 4u;
     for (int t = tile0; t < num_tiles && alive; t += tstride) {
       const int m = (t % num_m) * TILE_M + static_cast<int>(rank) * BM + q * 32 + lane;
       const int nh = (t / num_m) * BN + h * C::HALF;
       const bool row_ok = m < M;
       // the weight scales of the one or two blocks that the half-tile meets
-      // (past N: any block's, the sums are dropped), 32 groups at a time, one
-      // per lane
+      // (past N: any block's, the sums are dropped), one group per lane, a
+      // chunk ahead
       const int b0 = min(nh / kGroup, NB - 1), b1 = min((nh + C::HALF - 1) / kGroup, NB - 1);
       const float* sw0 = a.sw + static_cast<size_t>(b0) * G;
       const float* sw1 = a.sw + static_cast<size_t>(b1) * G;
-      float w0 = 0.0f, w1 = 0.0f;
+      auto weight_scale = [&](const float* p, int g) { return __ldg(p + min(g + lane, G - 1)); };
+      float w0n = weight_scale(sw0, 0), w1n = BN % 256 != 0 ? weight_scale(sw1, 0) : 0.0f;
       const int cross = (b0 + 1) * kGroup - nh;  // first column of the second block
       uint64_t acc[C::HALF / 2];
 #pragma unroll
@@ -340,49 +364,54 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       // (the row's scales come through shared memory: with the next ones on
       // their way from global memory, tcgen05.wait::ld waited for them too)
-      const float* sxl = sx_s + q * 32 + lane;
-      bool ready = false;  // this group's barriers were complete when polled during the last one
-      float x = 0.0f;
+      bool ready = false;  // the next group was complete when polled during the last one
 #pragma unroll 1
-      for (int g = 0; g < G; ++g, ++it) {
-        const uint32_t buf = it & 1u;
-        if ((g & 31) == 0) {
-          w0 = __ldg(sw0 + min(g + lane, G - 1));
-          if constexpr (BN % 256 != 0) w1 = __ldg(sw1 + min(g + lane, G - 1));
-        }
-        if (!__all_sync(0xffffffffu, ready)) {
-          alive = mbar_wait2_warp(&tfull[buf], (it >> 1) & 1u, &sfull[it % SX_RING], (it / SX_RING) & 1u, tmo,
-                                  abort_flag);
-          if (!alive) break;
-          x = sxl[(it % SX_RING) * BM];
-        }
-        tc_fence_after();
-        const uint32_t t = t_row + buf * SLOT_COLS;
-        uint32_t ra[32], rb[32];
-        tmem_ld_32x32b_x32(t, ra);
-        const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, g & 31)));
-        const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, g & 31))) : s0;
-        ready = false;
+      for (int g0 = 0; g0 < G && alive; g0 += SX_CHUNK, ++chunk) {
+        const float w0 = w0n, w1 = w1n;
+        w0n = weight_scale(sw0, g0 + SX_CHUNK);
+        if constexpr (BN % 256 != 0) w1n = weight_scale(sw1, g0 + SX_CHUNK);
+        alive = __all_sync(0xffffffffu, mbar_wait(&sfull[chunk & 1u], (chunk >> 1) & 1u, tmo, abort_flag));
+        uint32_t sx = sx0 + (chunk & 1u) * (SX_CHUNK * BM * 4);
+        const int n = min(SX_CHUNK, G - g0);
+#pragma unroll 1
+        for (int j = 0; j < n && alive; j += 2, sx += 2 * BM * 4, ph ^= 1u) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          uint32_t(&r)[32] = (c & 1) ? rb : ra;
-          uint32_t(&n)[32] = (c & 1) ? ra : rb;
-          tmem_wait_cols(r);
-          if (c + 1 < CH) {
-            tmem_ld_32x32b_x32(t + static_cast<uint32_t>((c + 1) * 32), n);
-          } else {  // the buffer is read: hand it back to the leader
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
-            if (g + 1 < G) {  // look ahead while the last columns are added
-              const uint32_t j = it + 1;
-              ready = mbar_test_wait(&tfull[j & 1u], (j >> 1) & 1u) &
-                      mbar_test_wait(&sfull[j % SX_RING], (j / SX_RING) & 1u);
-              x = sxl[(j % SX_RING) * BM];
+          for (int u = 0; u < 2; ++u) {
+            if (!__all_sync(0xffffffffu, ready))
+              alive = alive && mbar_wait2_warp(&tfull[u], ph, &tfull[u], ph, tmo, abort_flag);
+            tc_fence_after();
+            if (u == 0 || j + 1 < n) {
+              const uint32_t t = t_row + u * SLOT_COLS;
+              uint32_t ra[32], rb[32];
+              tmem_ld_32x32b_x32(t, ra);
+              const float x = lds_f32(sx + u * (BM * 4));
+              const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, j + u)));
+              const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, j + u))) : s0;
+#pragma unroll
+              for (int c = 0; c < CH; ++c) {
+                uint32_t(&r)[32] = (c & 1) ? rb : ra;
+                uint32_t(&nx)[32] = (c & 1) ? ra : rb;
+                tmem_wait_cols(r);
+                if (c + 1 < CH) {
+                  tmem_ld_32x32b_x32(t + static_cast<uint32_t>((c + 1) * 32), nx);
+                } else {  // the buffer is read: hand it back to the leader
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + u * 8u);
+                }
+                if (c == CH - 2) ready = mbar_test_wait(tfull0 + (u ^ 1) * 8u, u == 0 ? ph : ph ^ 1u);
+                add(r, c, s0, s1);
+              }
+            } else {  // the empty group of an odd tile
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + u * 8u);
+              ready = false;
             }
           }
-          add(r, c, s0, s1);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[chunk & 1u]);
       }
       if (!alive) {
         if (lane == 0) gfail(a, abort_flag);

@@ -65,14 +65,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -86,8 +86,17 @@ __device__ __forceinline__ bool mbar_wait2_warp(uint64_t* bar0, uint32_t parity0
                                                 uint64_t timeout_ns, volatile int* abort) {
 #pragma unroll 1
   for (int i = 0; i < 4096; ++i) {
-    const bool a = mbar_test_wait(bar0, parity0), b = mbar_test_wait(bar1, parity1);
-    if (__all_sync(0xffffffffu, a & b)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
   }
   return __all_sync(0xffffffffu,
                     mbar_wait(bar0, parity0, timeout_ns, abort) && mbar_wait(bar1, parity1, timeout_ns, abort));
