@@ -103,9 +103,11 @@ int8mm_status check_m(int64_t M) {
   return INT8MM_OK;
 }
 
-// 2-D array of bytes [rows, inner] (inner contiguous), 128-byte swizzled boxes
-// of 128 bytes x box_rows, zero fill outside.
-int8mm_status make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+// 2-D array [rows, inner] (inner contiguous, rows `pitch` bytes apart), boxes
+// of box_rows x box_inner, zero fill outside: bytes with the 128-byte swizzle,
+// or floats without.
+int8mm_status make_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
+                        uint64_t pitch, uint32_t box_inner, uint32_t box_rows) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -114,10 +116,11 @@ int8mm_status make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? p : nullptr);
   }();
   if (fn == nullptr) return fail(INT8MM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner};
-  const cuuint32_t box[2] = {kGroup, box_rows}, estr[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims[2] = {inner, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_inner, box_rows}, estr[2] = {1, 1};
+  const CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? INT8MM_OK
                            : fail(INT8MM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -372,14 +375,18 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
   a.bf16 = dtype == INT8MM_DTYPE_BF16;
   a.status = h->status;
   a.timeout_ns = h->timeout_ns;
-  CUtensorMap tmX, tmW;
+  CUtensorMap tmX, tmW, tmS;
   const int width = block_pair_width(M, N, h->num_sms);
-  if ((st = make_tmap(&tmX, codes_dev, static_cast<uint64_t>(K), static_cast<uint64_t>(M), 128)) != INT8MM_OK ||
-      (st = make_tmap(&tmW, h->Wb, kGroup, static_cast<uint64_t>(block_groups(K) * h->N_pad),
-                      static_cast<uint32_t>(width / 2))) != INT8MM_OK)
+  const uint64_t G = static_cast<uint64_t>(block_groups(K));
+  if ((st = make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes_dev, static_cast<uint64_t>(K),
+                      static_cast<uint64_t>(M), static_cast<uint64_t>(K), kGroup, 128)) != INT8MM_OK ||
+      (st = make_tmap(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, h->Wb, kGroup, G * static_cast<uint64_t>(h->N_pad), kGroup,
+                      kGroup, static_cast<uint32_t>(width / 2))) != INT8MM_OK ||
+      (st = make_tmap(&tmS, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, scales_dev, static_cast<uint64_t>(M), G,
+                      static_cast<uint64_t>(lds) * 4, 128, kSxChunk)) != INT8MM_OK)
     return st;
   const cudaError_t e =
-      launch_block_gemm_pair(tmX, tmW, a, width, h->num_sms, static_cast<cudaStream_t>(stream));
+      launch_block_gemm_pair(tmX, tmW, tmS, a, width, h->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "block-scaled product launch");
 }
 

@@ -13,9 +13,9 @@
 // X and BN / 2 rows of W per group (TMA, 128-byte swizzle, completing on the
 // leader's barrier), keeps its 128 rows of P_g in its own TMEM, sums and
 // writes them.  No multicast.
-//   warp 0      TMA producer
-//   warp 1      allocates TMEM; in the leader one lane issues the MMAs of a
-//               group (4 of 256 x BN x 32), alternating between two buffers
+//   warps 0, 3  TMA producers, one for X, one for W
+//   warps 1, 2  in the leader, issue the MMAs of every second group each (4 of
+//               256 x BN x 32), round-robin over the TMEM buffers
 //   warps 4-11  two per TMEM lane quarter, one row per thread and half of the
 //               tile's columns: they add P_g times sx sw to BN / 2 registers
 //               and write Y at the tile's end, while the next tile's first
@@ -52,34 +52,35 @@ constexpr int TILE_M = 256;
 constexpr int BM = 128;  // rows per CTA
 constexpr int EPI_WARPS = 8;
 // Three warpgroups, so that registers can move between them: launched with
-// 168 each (384 x 168 = 64512), the first (producer, MMA issuer, two idle
-// warps) goes down to 40 and the two epilogue groups up to 232
+// 168 each (384 x 168 = 64512), the first (two producers, two MMA
+// issuers) goes down to 40 and the two epilogue groups up to 232
 // (128 x 40 + 256 x 232 = 64512).
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int REGS_LAUNCH = 168, REGS_FRONT = 40, REGS_EPI = 232;
 static_assert(128 * REGS_FRONT + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS_LAUNCH, "registers within the launch's");
 
-// TMEM: two buffers of 256 columns.
-constexpr int SLOTS = 2, SLOT_COLS = 256;
-
 // Scales of a CTA's rows come up to SX_CHUNK groups of one tile at a time, two
 // chunks in turn.
-constexpr int SX_CHUNK = 16;
+constexpr int SX_CHUNK = kSxChunk;
 
 template <int BN>
 struct PCfg {
   static constexpr int A_BYTES = BM * kGroup;
   static constexpr int B_BYTES = BN / 2 * kGroup;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 204800 / STAGE;
+  static constexpr int STAGES = 212992 / STAGE;
   static constexpr int HALF = BN / 2;  // columns per epilogue warp
-  static constexpr int NBARS = 2 * STAGES + 2 * SLOTS + 1 + 4;
+  static constexpr int BUFS = 512 / BN;  // accumulator buffers in TMEM
+  static constexpr int ISSUERS = 2;  // warps that issue MMAs, group by group in turn
+  static constexpr bool CROSS = HALF != 64 && HALF != 128;  // a half may meet two blocks of the weight scales
+  static constexpr int CW = HALF <= 80 ? HALF : HALF == 96 ? 48 : 32;  // columns per TMEM read
+  static constexpr int NBARS = 2 * STAGES + 2 * BUFS + ISSUERS + 4;
   static constexpr int SX_OFF = STAGES * STAGE;
   static constexpr int BAR_OFF = SX_OFF + 2 * SX_CHUNK * BM * 4;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;  // + slack to align the base to 1024
   static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, BN);  // e4m3 and fp16 operands share the encoding 0
-  static_assert(HALF % 32 == 0 && BN <= SLOT_COLS && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
+  static_assert(CW % 16 == 0 && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
 };
 
 // D[tmem of both CTAs] (+)= A * B^T over the pair's shared memory, e4m3 to fp32.
@@ -98,14 +99,6 @@ __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r;
-}
-// Untiled copy of `bytes` (a multiple of 16) to shared memory, counted on
-// this CTA's barrier.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
 }
 __device__ __forceinline__ uint64_t make_desc(uint32_t lo, uint32_t hi) {
   return (static_cast<uint64_t>(hi) << 32) | lo;
@@ -148,28 +141,53 @@ __device__ __forceinline__ float lds_f32(uint32_t addr) {
   return v;
 }
 
-// Waits for this thread's TMEM reads.  The registers they fill go through the
-// statement, so that no use of them can move above it.
-__device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
+// W columns of this thread's TMEM lane, and the wait for them.  The
+// registers go through the wait, so that no use of them can move above it.
+template <int W>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[W]) {
+#pragma unroll
+  for (int c = 0; c + 32 <= W; c += 32) tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
+  if constexpr (W % 32 != 0) tmem_ld_32x32b_x16(taddr + W / 32 * 32, &r[W / 32 * 32]);
+}
+template <int W>
+__device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[W]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < W; i += 16)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                 "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])::"memory");
+}
+
+// Polls a barrier without suspending, the whole warp together (see
+// mbar_wait2_warp).
+__device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, unsigned long long tmo,
+                                               volatile int* abort_flag) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    if ((i & 4095u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t0 > tmo)) return false;
+    }
+  }
 }
 
 template <int BN, typename TY>
 __global__ void __launch_bounds__(THREADS, 1)
     block_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                           const BlockGemmArgs a) {
+                           const __grid_constant__ CUtensorMap tmS, const BlockGemmArgs a) {
   using C = PCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
-  uint64_t* tempty = tfull + SLOTS;
-  uint64_t* drain = tempty + SLOTS;
-  uint64_t* sfull = drain + 1;
+  uint64_t* tempty = tfull + C::BUFS;
+  uint64_t* drain = tempty + C::BUFS;
+  uint64_t* sfull = drain + C::ISSUERS;
   uint64_t* sempty = sfull + 2;
   float* sx_s = reinterpret_cast<float*>(smem + C::SX_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
@@ -183,18 +201,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int num_m = (M + TILE_M - 1) / TILE_M;
   const int num_tiles = num_m * ((N + BN - 1) / BN);
   const int G = (a.K + kGroup - 1) / kGroup;
-  const int G2 = (G + 1) & ~1;  // groups are taken in pairs, one per TMEM buffer
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < SLOTS; ++b) {
+    for (int b = 0; b < C::BUFS; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], EPI_WARPS * 2);
     }
-    mbar_init(drain, 1);
+    for (int s = 0; s < C::ISSUERS; ++s) mbar_init(&drain[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&sempty[s], EPI_WARPS);
@@ -203,6 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbar_init();
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmS);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -216,46 +234,44 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < 4) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FRONT));
-   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------ TMA producer
+   if (warp == 0 || warp == 3) {
+      // ----------------------------------------------------- TMA producers
+      // Warp 0 loads X and its scales, warp 3 W: issuing both takes one warp
+      // longer than a group's MMAs take the tensor cores.  Both CTAs' loads
+      // complete on the leader's barrier; its warp 0 announces the pair's
+      // bytes.
+      const bool is_x = warp == 0;
+      const uint32_t issuer = elect_one();
+      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
       int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_phase = 0, chunk = 0;
+      uint32_t phase = 1, chunk = 0;
       bool ok = true;
       const uint64_t pol_x = l2_policy_evict_last();  // every column tile of its rows reads X again
       for (int t = tile0; t < num_tiles && ok; t += tstride) {
         const int m0 = (t % num_m) * TILE_M + static_cast<int>(rank) * BM;
-        const int n0 = (t / num_m) * BN + static_cast<int>(rank) * (BN / 2);
-        // rows of scales: up to lds, a multiple of 4 (16 bytes)
-        const uint32_t sx_bytes = static_cast<uint32_t>(max(0, min(BM, (M - m0 + 3) & ~3))) * 4u;
-        for (int g = 0; g < G; ++g) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, tmo, abort_flag) ||
-              (g % SX_CHUNK == 0 && !mbar_wait(&sempty[chunk & 1u], ((chunk >> 1) & 1u) ^ 1u, tmo, abort_flag))) {
-            ok = false;
-            break;
-          }
-          // both CTAs' loads complete on the leader's barrier; the leader
-          // announces the pair's bytes
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE);
-          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-          uint8_t* st = smem + stage * C::STAGE;
-          tma_load_2d_pair_hint(st, &tmX, bar, g * kGroup, m0, pol_x);
-          tma_load_2d_pair(st + C::A_BYTES, &tmW, bar, 0, g * a.N_pad + n0);
-          if (g % SX_CHUNK == 0) {
-            uint64_t* sb = &sfull[chunk & 1u];
-            float* dst = sx_s + (chunk & 1u) * (SX_CHUNK * BM);
-            const int n = min(SX_CHUNK, G - g);
-            if (sx_bytes != 0u) {
-              mbar_arrive_expect_tx(sb, sx_bytes * static_cast<uint32_t>(n));
-              for (int j = 0; j < n; ++j)
-                bulk_load(dst + j * BM, a.sx + static_cast<size_t>(g + j) * a.lds + m0, sx_bytes, sb);
-            } else {
-              mbar_arrive(sb);
+        int w_row = (t / num_m) * BN + static_cast<int>(rank) * (BN / 2);
+        for (int g = 0; g < G && ok; ++g, w_row += a.N_pad) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, tmo, abort_flag));
+          if (ok && is_x && g % SX_CHUNK == 0) {
+            // the scales of up to 16 groups of this CTA's rows, one box
+            ok = __all_sync(0xffffffffu, mbar_wait(&sempty[chunk & 1u], ((chunk >> 1) & 1u) ^ 1u, tmo, abort_flag));
+            if (ok && issuer) {
+              mbar_arrive_expect_tx(&sfull[chunk & 1u], SX_CHUNK * BM * 4);
+              tma_load_2d(sx_s + (chunk & 1u) * (SX_CHUNK * BM), &tmS, &sfull[chunk & 1u], m0, g);
             }
             ++chunk;
           }
-          issued_mask |= 1u << stage;
-          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (ok && issuer) {
+            uint8_t* st = smem + stage * C::STAGE;
+            const uint32_t bar = full0 + static_cast<uint32_t>(stage) * 8u;
+            if (is_x) {
+              if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE);
+              tma_load_2d_pair_hint(st, &tmX, bar, g * kGroup, m0, pol_x);
+            } else {
+              tma_load_2d_pair(st + C::A_BYTES, &tmW, bar, 0, w_row);
+            }
+          }
+          __syncwarp();
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -263,67 +279,57 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) {
-        gfail(a, abort_flag);
-        for (uint32_t j = chunk > 2 ? chunk - 2 : 0; j < chunk; ++j)
-          mbar_wait(&sfull[j & 1u], (j >> 1) & 1u, tmo, nullptr);
-        // every load already issued lands before the CTA can exit (the peer
-        // cannot watch the leader's barriers: it waits a while)
-        if (rank == 0) {
-          for (int s = 0; s < C::STAGES; ++s)
-            if (issued_mask & (1u << s)) mbar_wait(&full[s], (issued_phase >> s) & 1u, tmo, nullptr);
-        } else {
-          const uint64_t t0 = global_timer_ns();
-          while (global_timer_ns() - t0 < 200000ull) {
-          }
+        // the loads already issued land, microseconds later, before the CTA exits
+        if (issuer) gfail(a, abort_flag);
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) {
         }
       }
-    }
-   } else if (warp == 1) {
+   } else if (warp <= C::ISSUERS) {
     if (rank == 0) {
-      // -------------------------------------------------------- MMA issuer
-      // The whole warp walks the loop and one elected lane issues: the
-      // descriptors then stay in uniform registers.
+      // ------------------------------------------------------- MMA issuers
+      // Every ISSUERS-th group: a group's waits and issue take one warp longer
+      // than its MMAs take the tensor cores.  The whole warp walks the loop
+      // and one elected lane issues: the descriptors then stay in uniform
+      // registers.
       const uint32_t issuer = elect_one();
       const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_k_sw128(0) >> 32);
       const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_k_sw128(smem_u32(smem)));
-      int stage = 0;
-      uint32_t phase = 0, it = 0;
+      int stage = warp - 1, buf = warp - 1;
+      uint32_t phase = 0, bphase = 1;
       bool ok = true;
-      for (int t = tile0; t < num_tiles && ok; t += tstride) {
-        for (int g = 0; g < G2 && ok; ++g, ++it) {
-          const uint32_t buf = it & 1u;
-          if (g == G) {  // an odd tile's last group is empty: no MMAs, only the commit
-            ok = mbar_wait2_warp(&tempty[buf], ((it >> 1) & 1u) ^ 1u, &tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo,
-                                 abort_flag);
-            if (ok && issuer) mma_commit_pair(&tfull[buf], 0x3);
-            __syncwarp();
-            continue;
-          }
-          ok = mbar_wait2_warp(&full[stage], phase, &tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag);
-          if (ok) {
-            tc_fence_after();
-            if (issuer) {
-              const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
-              const uint32_t bd = ad + (C::A_BYTES >> 4);
-              const uint32_t d = tmem_base + buf * SLOT_COLS;
+      int my_tiles = tile0 < num_tiles ? (num_tiles - tile0 + tstride - 1) / tstride : 0;
+      for (long long it = warp - 1; it < static_cast<long long>(my_tiles) * G && ok; it += C::ISSUERS) {
+        ok = mbar_wait2_warp(&full[stage], phase, &tempty[buf], bphase, tmo, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          if (issuer) {
+            const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
+            const uint32_t bd = ad + (C::A_BYTES >> 4);
+            const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
 #pragma unroll
-              for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
-                mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
-              mma_commit_pair(&tfull[buf], 0x3);
-              mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
+              mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
+            mma_commit_pair(&tfull[buf], 0x3);
+            mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
           }
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          __syncwarp();
+        }
+        buf += C::ISSUERS;
+        if (buf >= C::BUFS) {
+          buf -= C::BUFS;
+          bphase ^= 1u;
+        }
+        stage += C::ISSUERS;
+        if (stage >= C::STAGES) {
+          stage -= C::STAGES;
+          phase ^= 1u;
         }
       }
       if (!ok && issuer) {
         gfail(a, abort_flag);
-        mma_commit_pair(drain, 0x1);
-        mbar_wait(drain, 0, tmo, nullptr);
+        mma_commit_pair(&drain[warp - 1], 0x1);
+        mbar_wait(&drain[warp - 1], 0, tmo, nullptr);
       }
     }
    }
@@ -334,9 +340,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int h = (warp - 4) >> 2;      // half of the tile's columns
     const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
-    constexpr int CH = C::HALF / 32;
     const int NB = (N + kGroup - 1) / kGroup;
-    uint32_t chunk = 0, ph = 0;
+    uint32_t chunk = 0, buf = 0, ph = 0;
     bool alive = true;
     const uint32_t tfull0 = smem_u32(&tfull[0]);
     const uint32_t sx0 = smem_u32(sx_s) + static_cast<uint32_t>(q * 32 + lane) * 4u;
@@ -351,17 +356,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float* sw0 = a.sw + static_cast<size_t>(b0) * G;
       const float* sw1 = a.sw + static_cast<size_t>(b1) * G;
       auto weight_scale = [&](const float* p, int g) { return __ldg(p + min(g + lane, G - 1)); };
-      float w0n = weight_scale(sw0, 0), w1n = BN % 256 != 0 ? weight_scale(sw1, 0) : 0.0f;
+      float w0n = weight_scale(sw0, 0), w1n = weight_scale(sw1, 0);
       const int cross = (b0 + 1) * kGroup - nh;  // first column of the second block
       uint64_t acc[C::HALF / 2];
 #pragma unroll
       for (int i = 0; i < C::HALF / 2; ++i) acc[i] = 0ull;
-      // columns [32 c, 32 c + 32) of the warp's half-tile += r times the scale
-      auto add = [&](const uint32_t (&r)[32], int c, uint64_t s0, uint64_t s1) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          fma2(acc[c * 16 + i], r[2 * i], r[2 * i + 1], (BN % 256 != 0 && c * 32 >= cross) ? s1 : s0);
-      };
       // (the row's scales come through shared memory: with the next ones on
       // their way from global memory, tcgen05.wait::ld waited for them too)
       bool ready = false;  // the next group was complete when polled during the last one
@@ -369,45 +368,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int g0 = 0; g0 < G && alive; g0 += SX_CHUNK, ++chunk) {
         const float w0 = w0n, w1 = w1n;
         w0n = weight_scale(sw0, g0 + SX_CHUNK);
-        if constexpr (BN % 256 != 0) w1n = weight_scale(sw1, g0 + SX_CHUNK);
+        w1n = weight_scale(sw1, g0 + SX_CHUNK);
         alive = __all_sync(0xffffffffu, mbar_wait(&sfull[chunk & 1u], (chunk >> 1) & 1u, tmo, abort_flag));
         uint32_t sx = sx0 + (chunk & 1u) * (SX_CHUNK * BM * 4);
         const int n = min(SX_CHUNK, G - g0);
 #pragma unroll 1
-        for (int j = 0; j < n && alive; j += 2, sx += 2 * BM * 4, ph ^= 1u) {
+        for (int j = 0; j < n && alive; ++j, sx += BM * 4) {
+          if (!__all_sync(0xffffffffu, ready)) alive = mbar_wait_poll(tfull0 + buf * 8u, ph, tmo, abort_flag);
+          tc_fence_after();
+          const uint32_t tb = t_row + buf * BN;
+          uint32_t r[C::CW];
+          tmem_ld_cols<C::CW>(tb, r);
+          const float x = lds_f32(sx);
+          const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, j)));
+          const uint64_t s1 = C::CROSS ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, j))) : s0;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (!__all_sync(0xffffffffu, ready))
-              alive = alive && mbar_wait2_warp(&tfull[u], ph, &tfull[u], ph, tmo, abort_flag);
-            tc_fence_after();
-            if (u == 0 || j + 1 < n) {
-              const uint32_t t = t_row + u * SLOT_COLS;
-              uint32_t ra[32], rb[32];
-              tmem_ld_32x32b_x32(t, ra);
-              const float x = lds_f32(sx + u * (BM * 4));
-              const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, j + u)));
-              const uint64_t s1 = BN % 256 != 0 ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, j + u))) : s0;
-#pragma unroll
-              for (int c = 0; c < CH; ++c) {
-                uint32_t(&r)[32] = (c & 1) ? rb : ra;
-                uint32_t(&nx)[32] = (c & 1) ? ra : rb;
-                tmem_wait_cols(r);
-                if (c + 1 < CH) {
-                  tmem_ld_32x32b_x32(t + static_cast<uint32_t>((c + 1) * 32), nx);
-                } else {  // the buffer is read: hand it back to the leader
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + u * 8u);
-                }
-                if (c == CH - 2) ready = mbar_test_wait(tfull0 + (u ^ 1) * 8u, u == 0 ? ph : ph ^ 1u);
-                add(r, c, s0, s1);
-              }
-            } else {  // the empty group of an odd tile
+          for (int c = 0; c < C::HALF; c += C::CW) {
+            if (c > 0) tmem_ld_cols<C::CW>(tb + c, r);
+            tmem_wait_cols<C::CW>(r);
+            if (c + C::CW == C::HALF) {  // the buffer is read: hand it back to the leader
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + u * 8u);
-              ready = false;
+              if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
+              if (++buf == C::BUFS) {
+                buf = 0;
+                ph ^= 1u;
+              }
+              ready = mbar_test_wait(tfull0 + buf * 8u, ph);
             }
+#pragma unroll
+            for (int i = 0; i < C::CW / 2; ++i)
+              fma2(acc[c / 2 + i], r[2 * i], r[2 * i + 1], (C::CROSS && ((c + 2 * i) & ~15) >= cross) ? s1 : s0);
           }
         }
         __syncwarp();
@@ -465,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int BN, typename TY>
-cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const BlockGemmArgs& a, int num_sms,
+cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS, const BlockGemmArgs& a, int num_sms,
                         cudaStream_t stream) {
   auto kern = block_gemm_pair_kernel<BN, TY>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<BN>::SMEM);
@@ -483,7 +474,7 @@ cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const Bl
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tmX, tmW, a);
+  return cudaLaunchKernelEx(&cfg, kern, tmX, tmW, tmS, a);
 }
 
 }  // namespace
@@ -505,14 +496,15 @@ int block_pair_width(int64_t M, int64_t N, int num_sms) {
   return best;
 }
 
-cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const BlockGemmArgs& a, int width,
+cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS, const BlockGemmArgs& a, int width,
                                    int num_sms, cudaStream_t stream) {
 #define PAIR(W)                                                                    \
   if (width == W)                                                                  \
-    return a.bf16 ? launch_pair<W, __nv_bfloat16>(tmX, tmW, a, num_sms, stream)    \
-                  : launch_pair<W, __half>(tmX, tmW, a, num_sms, stream)
+    return a.bf16 ? launch_pair<W, __nv_bfloat16>(tmX, tmW, tmS, a, num_sms, stream)    \
+                  : launch_pair<W, __half>(tmX, tmW, tmS, a, num_sms, stream)
   PAIR(256);
   PAIR(192);
+  PAIR(160);
   PAIR(128);
 #undef PAIR
   return cudaErrorInvalidValue;
