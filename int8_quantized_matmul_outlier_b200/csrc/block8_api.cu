@@ -28,6 +28,7 @@ struct int8mm_block_weight {
   int64_t K = 0, N = 0, N_pad = 0;
   uint8_t* Wb = nullptr;  // [G][N_pad][128] codes
   float* sw = nullptr;    // [N / 128][G]
+  RowsPlan rows = {1, 1};  // split of products of few rows
   int* status = nullptr;
   unsigned long long timeout_ns = 2000000000ull;
   size_t bytes = 0;
@@ -201,6 +202,9 @@ int8mm_status prepare(const void* W, int dtype, const float* scales, int64_t K, 
   h->K = K;
   h->N = N;
   h->N_pad = N_pad;
+  int clusters[4] = {};
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = rows_max_clusters(1 << i, &clusters[i]);
+  h->rows = rows_plan(N, K, clusters);
   const size_t nsw = static_cast<size_t>((N + kGroup - 1) / kGroup * G);
   const size_t nwb = static_cast<size_t>(G * N_pad) * kGroup;
   if (e == cudaSuccess) e = cudaMallocAsync(reinterpret_cast<void**>(&h->Wb), nwb, s);
@@ -375,18 +379,27 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
   a.bf16 = dtype == INT8MM_DTYPE_BF16;
   a.status = h->status;
   a.timeout_ns = h->timeout_ns;
-  CUtensorMap tmX, tmW, tmS;
-  const int width = block_pair_width(M, N, h->num_sms);
-  const uint64_t G = static_cast<uint64_t>(block_groups(K));
-  if ((st = make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes_dev, static_cast<uint64_t>(K),
-                      static_cast<uint64_t>(M), static_cast<uint64_t>(K), kGroup, 128)) != INT8MM_OK ||
-      (st = make_tmap(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, h->Wb, kGroup, G * static_cast<uint64_t>(h->N_pad), kGroup,
-                      kGroup, static_cast<uint32_t>(width / 2))) != INT8MM_OK ||
-      (st = make_tmap(&tmS, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, scales_dev, static_cast<uint64_t>(M), G,
-                      static_cast<uint64_t>(lds) * 4, 128, kSxChunk)) != INT8MM_OK)
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool few = M <= kRowsMaxM;
+  const int width = few ? 0 : block_pair_width(M, N, h->num_sms);
+  const uint32_t box_m = few ? static_cast<uint32_t>(rows_padded_tokens(M)) : 128u;
+  const uint64_t G = static_cast<uint64_t>(block_groups(K)), w_rows = G * static_cast<uint64_t>(h->N_pad);
+  constexpr CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  CUtensorMap tmX, tmW, tmS, tmW16;
+  if ((st = make_tmap(&tmX, u8, codes_dev, static_cast<uint64_t>(K), static_cast<uint64_t>(M),
+                      static_cast<uint64_t>(K), kGroup, box_m)) != INT8MM_OK ||
+      (st = make_tmap(&tmW, u8, h->Wb, kGroup, w_rows, kGroup, kGroup,
+                      few ? 128u : static_cast<uint32_t>(width / 2))) != INT8MM_OK ||
+      (st = make_tmap(&tmS, f32, scales_dev, static_cast<uint64_t>(M), G, static_cast<uint64_t>(lds) * 4, box_m,
+                      kSxChunk)) != INT8MM_OK)
     return st;
-  const cudaError_t e =
-      launch_block_gemm_pair(tmX, tmW, tmS, a, width, h->num_sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e;
+  if (few) {
+    if ((st = make_tmap(&tmW16, u8, h->Wb, kGroup, w_rows, kGroup, kGroup, 16)) != INT8MM_OK) return st;
+    e = launch_block_gemm_rows(tmW, tmW16, tmX, tmS, a, h->rows, s);
+  } else {
+    e = launch_block_gemm_pair(tmX, tmW, tmS, a, width, h->num_sms, s);
+  }
   return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "block-scaled product launch");
 }
 

@@ -1,0 +1,503 @@
+// Matrix product of e4m3 codes with block scales for few rows (tokens), sm_100a:
+//
+//   Y[m, n] = sum_g sx[g][m] sw[n / 128][g] P_g[m, n]  (+ bias[n])
+//   P_g[m, n] = sum_{k in g} X[m, k] W[n, k]
+//
+// Bound by reading W once.  The operands are swapped: 128 rows of W (columns n
+// of Y) take the MMA's M slot and the MP padded tokens its N slot; P_g comes
+// from the tensor cores (tcgen05.mma kind::f8f6f4) and is added to fp32
+// registers with its factor, as in the kernel for many rows.
+//
+// Work split: a cluster of S CTAs takes a run of W's rows, in 16s, so that all
+// clusters' runs are equal within 16 rows; its CTAs take equal parts of the
+// groups of K.  Each tile's S partial sums meet in shared memory of the
+// cluster: CTA r finishes the tokens [r MP / S, (r + 1) MP / S), adding the S
+// parts in the order of the ranks.  No workspace, no atomics, and the same
+// result every time.  Splitting N alone would leave SMs idle at small N and
+// the last round part-filled; splitting K alone would need the sum in memory.
+//   warp 0      TMA producer (W marked evict-first in L2), GS groups per stage
+//   warp 1      TMEM, MMA issuer
+//   warps 4..   sums: one row n per thread; with 64 or more tokens two warps
+//               share a TMEM lane quarter, half of the tokens each
+// Two groups per stage for up to 64 tokens: a step's waits take each of these
+// warps some 500 cycles, a group's 16 KB of W some 700 at the SM's share of
+// the HBM rate.
+//
+// Every wait is bounded; a timeout sets the status word, and the CTA drains
+// and exits with its cluster.
+#include "block8.cuh"
+#include "block8_gemm.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+#include <algorithm>
+
+namespace i8mm {
+namespace {
+
+constexpr int RM = 128;  // rows of W per tile
+constexpr int R_CHUNK = kSxChunk;
+
+template <int MP>
+struct RCfg {
+  static constexpr int GS = MP <= 64 ? 2 : 1;  // groups per stage
+  static constexpr int NH = MP >= 64 ? 2 : 1;  // token halves
+  static constexpr int TH = MP / NH;           // tokens per thread
+  static constexpr int EPI = 4 * NH;           // epilogue warps
+  static constexpr int THREADS = 128 + 32 * EPI;
+  static constexpr int W_BYTES = RM * kGroup, X_BYTES = MP * kGroup;
+  static constexpr int STAGE = GS * (W_BYTES + X_BYTES);
+  static constexpr int STAGES = MP <= 16 ? 5 : (MP <= 32 ? 4 : (MP <= 64 ? 3 : 4));
+  static constexpr int SX_OFF = STAGES * STAGE;             // [2][R_CHUNK][MP] scales
+  static constexpr int RED_OFF = SX_OFF + 2 * R_CHUNK * MP * 4;  // [S][MP / S][RM] partial sums
+  static constexpr int BAR_OFF = RED_OFF + MP * RM * 4;
+  static constexpr int NBARS = 2 * STAGES + 4 + 4 + 2 + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + 1024;
+  static constexpr int TMEM_COLS = 2 * GS * MP < 32 ? 32 : 2 * GS * MP;
+  static constexpr uint32_t IDESC = idesc_f16_f32(RM, MP);  // e4m3 and fp16 operands share the encoding 0
+  static_assert(STAGE % 1024 == 0 && X_BYTES % 1024 == 0 && SMEM <= 232448, "shared memory");
+  static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "TMEM allocation");
+};
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t relect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_nctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_id_x() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_count_x() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// mbar_wait for a phase that other CTAs of the cluster complete, with their
+// writes to this CTA's shared memory visible after it.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                                  volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 15) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort || now - t0 > timeout_ns) return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void rfail(const BlockGemmArgs& a, volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(a.status, kStatusTimeout);
+}
+
+// N columns of this thread's TMEM lane.
+template <int N>
+__device__ __forceinline__ void rows_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 16) {
+    tmem_ld_32x32b_x16(taddr, r);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
+  }
+}
+// Waits for them; the registers go through it, so that no use moves above it.
+template <int N>
+__device__ __forceinline__ void rows_wait(uint32_t (&r)[N]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; i += 16)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                 "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])::"memory");
+}
+
+// tmW: the weight's rows of 128 bytes with 128-row boxes; tmW16 with 16-row
+// boxes; tmX: the codes [M, K] with MP-row boxes; tmS: the scales [G][M] with
+// 16 x MP boxes.
+template <int MP, typename TY>
+__global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
+    block_gemm_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW16,
+                           const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS,
+                           const BlockGemmArgs a) {
+  using C = RCfg<MP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* sx_s = reinterpret_cast<float*>(smem + C::SX_OFF);
+  float* red_s = reinterpret_cast<float*>(smem + C::RED_OFF);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;  // [2]
+  uint64_t* tempty = tfull + 2;         // [2]
+  uint64_t* sfull = tempty + 2;         // [2]
+  uint64_t* sempty = sfull + 2;         // [2]
+  uint64_t* rfull = sempty + 2;         // the other CTAs' parts of my tokens are here
+  uint64_t* rempty = rfull + 1;         // the other CTAs have read my parts
+  uint64_t* drain = rempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int S = static_cast<int>(cluster_nctas()), rank = static_cast<int>(cluster_ctarank());
+  const int G = (a.K + kGroup - 1) / kGroup;
+  const int g_begin = G * rank / S, g_end = G * (rank + 1) / S;
+  const int steps = (g_end - g_begin + C::GS - 1) / C::GS;
+  const long long units = a.N / 16, nclus = cluster_count_x(), clus = cluster_id_x();
+  const int row_begin = static_cast<int>(units * clus / nclus) * 16;
+  const int row_end = static_cast<int>(units * (clus + 1) / nclus) * 16;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], C::EPI);
+      mbar_init(&sfull[b], 1);
+      mbar_init(&sempty[b], C::EPI);
+    }
+    mbar_init(rfull, static_cast<uint32_t>(max(1, (S - 1) * C::EPI)));
+    mbar_init(rempty, static_cast<uint32_t>(max(1, (S - 1) * C::EPI)));
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmS);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // the peers' barriers are initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const unsigned long long tmo = a.timeout_ns;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- TMA producer
+    const uint32_t issuer = relect_one();
+    const uint64_t pol_w = l2_policy_evict_first();  // W is read once
+    int stage = 0;
+    uint32_t phase = 1, chunk = 0;
+    bool ok = true;
+    for (int r0 = row_begin; r0 < row_end && ok; r0 += RM) {
+      const int rows = min(RM, row_end - r0);
+      for (int s = 0; s < steps && ok; ++s) {
+        const int g = g_begin + s * C::GS, n = min(C::GS, g_end - g);
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, tmo, abort_flag));
+        if (ok && s % (R_CHUNK / C::GS) == 0) {
+          // the scales of the next 16 groups, one box
+          ok = __all_sync(0xffffffffu, mbar_wait(&sempty[chunk & 1u], ((chunk >> 1) & 1u) ^ 1u, tmo, abort_flag));
+          if (ok && issuer) {
+            mbar_arrive_expect_tx(&sfull[chunk & 1u], R_CHUNK * MP * 4);
+            tma_load_2d(sx_s + (chunk & 1u) * (R_CHUNK * MP), &tmS, &sfull[chunk & 1u], 0, g);
+          }
+          ++chunk;
+        }
+        if (ok && issuer) {
+          uint8_t* st = smem + stage * C::STAGE;
+          mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(n * (rows * kGroup + C::X_BYTES)));
+          for (int u = 0; u < n; ++u) {
+            uint8_t* w = st + u * C::W_BYTES;
+            const int wr = (g + u) * a.N_pad + r0;
+            if (rows == RM) {
+              tma_load_2d_hint(w, &tmW, &full[stage], 0, wr, pol_w);
+            } else {
+              for (int i = 0; i < rows; i += 16) tma_load_2d_hint(w + i * kGroup, &tmW16, &full[stage], 0, wr + i, pol_w);
+            }
+            tma_load_2d(st + C::GS * C::W_BYTES + u * C::X_BYTES, &tmX, &full[stage], (g + u) * kGroup, 0);
+          }
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      // the loads already issued land, microseconds later, before the CTA exits
+      if (issuer) rfail(a, abort_flag);
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t issuer = relect_one();
+    const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_k_sw128(0) >> 32);
+    const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_k_sw128(smem_u32(smem)));
+    int stage = 0;
+    uint32_t phase = 0, it = 0;
+    bool ok = true;
+    for (int r0 = row_begin; r0 < row_end && ok; r0 += RM) {
+      for (int s = 0; s < steps && ok; ++s, ++it) {
+        const int n = min(C::GS, g_end - g_begin - s * C::GS);
+        const uint32_t buf = it & 1u;
+        ok = mbar_wait2_warp(&full[stage], phase, &tempty[buf], ((it >> 1) & 1u) ^ 1u, tmo, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          if (issuer) {
+            const uint32_t sd = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
+#pragma unroll
+            for (int u = 0; u < C::GS; ++u) {
+              if (u < n) {
+                const uint32_t ad = sd + u * (C::W_BYTES >> 4);
+                const uint32_t bd = sd + ((C::GS * C::W_BYTES + u * C::X_BYTES) >> 4);
+                const uint32_t d = tmem_base + (buf * C::GS + u) * MP;
+#pragma unroll
+                for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
+                  mma_e4m3(d, (static_cast<uint64_t>(desc_hi) << 32) | (ad + kk * 2),
+                           (static_cast<uint64_t>(desc_hi) << 32) | (bd + kk * 2), C::IDESC, kk != 0);
+              }
+            }
+            mma_commit(&tfull[buf]);
+            mma_commit(&empty[stage]);
+          }
+          __syncwarp();
+        }
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && issuer) {
+      rfail(a, abort_flag);
+      mma_commit(drain);
+      mbar_wait(drain, 0, tmo, nullptr);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------ sums and epilogue
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const int row = q * 32 + lane;  // of the tile
+    const int m0 = h * C::TH;       // first token
+    const int M = a.M, N = a.N;
+    const int NB = (N + kGroup - 1) / kGroup;
+    const int TS = MP / S;          // tokens that a CTA finishes
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(m0);
+    const uint32_t red0 = smem_u32(red_s);
+    uint32_t it = 0, chunk = 0, tile = 0;
+    bool alive = true;
+    for (int r0 = row_begin; r0 < row_end && alive; r0 += RM, ++tile) {
+      const int n = r0 + row;
+      const bool n_ok = n < row_end;
+      // scales of the one or two blocks that the tile's rows meet, 16 groups
+      // at a time: lanes 0-15 the first block's, 16-31 the second's
+      const int b0 = r0 / kGroup, b1 = min(b0 + 1, NB - 1);
+      const float* swp = a.sw + static_cast<size_t>(lane < 16 ? b0 : b1) * G;
+      const int sel = (n / kGroup != b0) ? 16 : 0;
+      auto weight_scale = [&](int g) { return __ldg(swp + min(g + (lane & 15), G - 1)); };
+      float wn = weight_scale(g_begin);
+      float acc[C::TH];
+#pragma unroll
+      for (int t = 0; t < C::TH; ++t) acc[t] = 0.0f;
+#pragma unroll 1
+      for (int g0 = g_begin; g0 < g_end && alive; g0 += R_CHUNK, ++chunk) {
+        const float w = wn;
+        wn = weight_scale(g0 + R_CHUNK);
+        alive = __all_sync(0xffffffffu, mbar_wait(&sfull[chunk & 1u], (chunk >> 1) & 1u, tmo, abort_flag));
+        const float* sx = sx_s + (chunk & 1u) * (R_CHUNK * MP) + m0;
+        const int ng = min(R_CHUNK, g_end - g0);
+#pragma unroll 1
+        for (int j = 0; j < ng && alive; j += C::GS, ++it) {
+          const uint32_t buf = it & 1u;
+          alive = mbar_wait2_warp(&tfull[buf], (it >> 1) & 1u, &tfull[buf], (it >> 1) & 1u, tmo, abort_flag);
+          if (!alive) break;
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < C::GS; ++u) {
+            uint32_t r[C::TH];
+            rows_ld<C::TH>(t_row + (buf * C::GS + u) * MP, r);  // of no use past ng, and not used
+            const float ws = __shfl_sync(0xffffffffu, w, sel + ((j + u) & 15));
+            rows_wait<C::TH>(r);
+            if (u == C::GS - 1) {  // the buffer is read: hand it back
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&tempty[buf]);
+            }
+            if (j + u < ng) {
+              const float4* s4 = reinterpret_cast<const float4*>(sx + (j + u) * MP);
+#pragma unroll
+              for (int t = 0; t < C::TH; t += 4) {
+                const float4 s = s4[t / 4];
+                acc[t + 0] = __fmaf_rn(__uint_as_float(r[t + 0]), __fmul_rn(s.x, ws), acc[t + 0]);
+                acc[t + 1] = __fmaf_rn(__uint_as_float(r[t + 1]), __fmul_rn(s.y, ws), acc[t + 1]);
+                acc[t + 2] = __fmaf_rn(__uint_as_float(r[t + 2]), __fmul_rn(s.z, ws), acc[t + 2]);
+                acc[t + 3] = __fmaf_rn(__uint_as_float(r[t + 3]), __fmul_rn(s.w, ws), acc[t + 3]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[chunk & 1u]);
+      }
+      // the tile's parts meet: token m at [rank][m % TS][row] of CTA m / TS
+      if (S > 1 && alive) {
+        if (tile > 0)
+          alive = __all_sync(0xffffffffu, mbar_wait_cluster(rempty, (tile - 1) & 1u, tmo, abort_flag));
+        if (alive) {
+          for (int c = 0; c < S; ++c) {
+            if (c == rank) continue;
+            const uint32_t dst = mapa_shared(red0 + static_cast<uint32_t>((rank * TS * RM + row) * 4), static_cast<uint32_t>(c));
+#pragma unroll
+            for (int t = 0; t < C::TH; ++t) {
+              const int k = m0 + t - c * TS;
+              if (k >= 0 && k < TS && m0 + t < M) st_cluster_f32(dst + static_cast<uint32_t>(k * RM * 4), acc[t]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0)
+            for (int c = 0; c < S; ++c)
+              if (c != rank) mbar_arrive_cluster(mapa_shared(smem_u32(rfull), static_cast<uint32_t>(c)));
+          alive = __all_sync(0xffffffffu, mbar_wait_cluster(rfull, tile & 1u, tmo, abort_flag));
+        }
+      }
+      if (!alive) {
+        if (lane == 0) rfail(a, abort_flag);
+        break;
+      }
+      const float bias = (n_ok && a.bias != nullptr) ? static_cast<float>(static_cast<const TY*>(a.bias)[n]) : 0.0f;
+#pragma unroll
+      for (int t = 0; t < C::TH; ++t) {
+        const int m = m0 + t, k = m - rank * TS;
+        if (k >= 0 && k < TS && m < M) {
+          float v = 0.0f;
+          for (int c = 0; c < S; ++c) v = __fadd_rn(v, c == rank ? acc[t] : red_s[(c * TS + k) * RM + row]);
+          v = __fadd_rn(v, bias);
+          if (n_ok) static_cast<TY*>(a.Y)[static_cast<size_t>(m) * N + n] = TY(v);
+        }
+      }
+      if (S > 1) {
+        __syncwarp();
+        if (lane == 0)
+          for (int c = 0; c < S; ++c)
+            if (c != rank) mbar_arrive_cluster(mapa_shared(smem_u32(rempty), static_cast<uint32_t>(c)));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peers may still write to it or signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <int MP, typename TY>
+cudaError_t configure_rows(int S, cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
+  auto kern = block_gemm_rows_kernel<MP, TY>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RCfg<MP>::SMEM);
+  if (e != cudaSuccess) return e;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = static_cast<unsigned>(S);
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(S));
+  cfg.blockDim = dim3(RCfg<MP>::THREADS);
+  cfg.dynamicSmemBytes = RCfg<MP>::SMEM;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaSuccess;
+}
+
+template <int MP, typename TY>
+cudaError_t launch_rows(const CUtensorMap& tmW, const CUtensorMap& tmW16, const CUtensorMap& tmX,
+                        const CUtensorMap& tmS, const BlockGemmArgs& a, const RowsPlan& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  const cudaError_t e = configure_rows<MP, TY>(p.split, cfg, &attr);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.split * p.clusters));
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, block_gemm_rows_kernel<MP, TY>, tmW, tmW16, tmX, tmS, a);
+}
+
+}  // namespace
+
+int rows_padded_tokens(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+
+// Clusters of S CTAs that fit the device at once, one CTA per SM.
+cudaError_t rows_max_clusters(int S, int* clusters) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cudaError_t e = configure_rows<128, __half>(S, cfg, &attr);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(clusters, block_gemm_rows_kernel<128, __half>, &cfg);
+  return e;
+}
+
+// Split of K and number of clusters: the least time of the fullest CTA, in
+// rows x groups, plus what a tile costs besides (its sums' meeting, about
+// 400 rows' time of one group per tile and CTA of the cluster).
+RowsPlan rows_plan(int64_t N, int64_t K, const int (&max_clusters)[4]) {
+  const int64_t units = N / 16, G = block_groups(K);
+  RowsPlan best{1, 1};
+  int64_t best_cost = -1;
+  for (int i = 0; i < 4; ++i) {
+    const int S = 1 << i;
+    if (S > G || max_clusters[i] < 1) continue;
+    const int64_t c = std::min<int64_t>(units, max_clusters[i]);
+    const int64_t rows = (units + c - 1) / c * 16, groups = (G + S - 1) / S;
+    const int64_t tiles = (rows + RM - 1) / RM;
+    const int64_t cost = std::max<int64_t>(rows, 48) * groups + tiles * (S > 1 ? 400 + 100 * S : 200);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = RowsPlan{S, static_cast<int>(c)};
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_block_gemm_rows(const CUtensorMap& tmW, const CUtensorMap& tmW16, const CUtensorMap& tmX,
+                                   const CUtensorMap& tmS, const BlockGemmArgs& a, const RowsPlan& p,
+                                   cudaStream_t stream) {
+#define ROWS(MP)                                                                              \
+  case MP:                                                                                    \
+    return a.bf16 ? launch_rows<MP, __nv_bfloat16>(tmW, tmW16, tmX, tmS, a, p, stream)        \
+                  : launch_rows<MP, __half>(tmW, tmW16, tmX, tmS, a, p, stream)
+  switch (rows_padded_tokens(a.M)) {
+    ROWS(16);
+    ROWS(32);
+    ROWS(64);
+    ROWS(128);
+  }
+#undef ROWS
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace i8mm
