@@ -12,14 +12,16 @@
 // clusters' runs are equal within 16 rows; its CTAs take equal parts of the
 // groups of K.  Each tile's S partial sums meet in shared memory of the
 // cluster: CTA r finishes the tokens [r MP / S, (r + 1) MP / S), adding the S
-// parts in the order of the ranks.  No workspace, no atomics, and the same
+// parts in the order of the ranks; the parts travel as one bulk copy per pair
+// of CTAs (stored value by value from the registers into the peers' memory,
+// 32 tokens at K = N = 8192 took 36.9 us, 14 more than one token).  No workspace, no atomics, and the same
 // result every time.  Splitting N alone would leave SMs idle at small N and
 // the last round part-filled; splitting K alone would need the sum in memory.
 //   warp 0      TMA producer (W marked evict-first in L2), GS groups per stage
 //   warp 1      TMEM, MMA issuer
 //   warps 4..   sums: one row n per thread; with 64 or more tokens two warps
 //               share a TMEM lane quarter, half of the tokens each
-// Two groups per stage for up to 64 tokens: a step's waits take each of these
+// Two groups per stage: a step's waits take each of these
 // warps some 500 cycles, a group's 16 KB of W some 700 at the SM's share of
 // the HBM rate.
 //
@@ -40,16 +42,17 @@ constexpr int R_CHUNK = kSxChunk;
 
 template <int MP>
 struct RCfg {
-  static constexpr int GS = MP <= 64 ? 2 : 1;  // groups per stage
+  static constexpr int GS = 2;                 // groups per stage
   static constexpr int NH = MP >= 64 ? 2 : 1;  // token halves
   static constexpr int TH = MP / NH;           // tokens per thread
   static constexpr int EPI = 4 * NH;           // epilogue warps
   static constexpr int THREADS = 128 + 32 * EPI;
   static constexpr int W_BYTES = RM * kGroup, X_BYTES = MP * kGroup;
   static constexpr int STAGE = GS * (W_BYTES + X_BYTES);
-  static constexpr int STAGES = MP <= 16 ? 5 : (MP <= 32 ? 4 : (MP <= 64 ? 3 : 4));
+  static constexpr int STAGES = MP <= 16 ? 5 : (MP <= 32 ? 4 : 3);
   static constexpr int SX_OFF = STAGES * STAGE;             // [2][R_CHUNK][MP] scales
-  static constexpr int RED_OFF = SX_OFF + 2 * R_CHUNK * MP * 4;  // [S][MP / S][RM] partial sums
+  static constexpr int OUT_OFF = SX_OFF + 2 * R_CHUNK * MP * 4;  // [MP][RM] this CTA's partial sums
+  static constexpr int RED_OFF = OUT_OFF + MP * RM * 4;          // [S][MP / S][RM] the others' of my tokens
   static constexpr int BAR_OFF = RED_OFF + MP * RM * 4;
   static constexpr int NBARS = 2 * STAGES + 4 + 4 + 2 + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
@@ -89,9 +92,14 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
   asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Copy of `bytes` (a multiple of 16) from this CTA's shared memory to a
+// cluster address, counted on the barrier there.
+__device__ __forceinline__ void bulk_to_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
+__device__ __forceinline__ void epi_sync(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
 
 // mbar_wait for a phase that other CTAs of the cluster complete, with their
 // writes to this CTA's shared memory visible after it.
@@ -154,6 +162,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sx_s = reinterpret_cast<float*>(smem + C::SX_OFF);
+  float* out_s = reinterpret_cast<float*>(smem + C::OUT_OFF);
   float* red_s = reinterpret_cast<float*>(smem + C::RED_OFF);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* empty = full + C::STAGES;
@@ -187,7 +196,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
       mbar_init(&sfull[b], 1);
       mbar_init(&sempty[b], C::EPI);
     }
-    mbar_init(rfull, static_cast<uint32_t>(max(1, (S - 1) * C::EPI)));
+    mbar_init(rfull, 1);
     mbar_init(rempty, static_cast<uint32_t>(max(1, (S - 1) * C::EPI)));
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -308,11 +317,12 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
     const int M = a.M, N = a.N;
     const int NB = (N + kGroup - 1) / kGroup;
     const int TS = MP / S;          // tokens that a CTA finishes
+    const int mine = max(0, min(TS, M - rank * TS));
     const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(m0);
-    const uint32_t red0 = smem_u32(red_s);
     uint32_t it = 0, chunk = 0, tile = 0;
     bool alive = true;
-    for (int r0 = row_begin; r0 < row_end && alive; r0 += RM, ++tile) {
+    // after a timeout a warp still takes part in the named barriers
+    for (int r0 = row_begin; r0 < row_end; r0 += RM, ++tile) {
       const int n = r0 + row;
       const bool n_ok = n < row_end;
       // scales of the one or two blocks that the tile's rows meet, 16 groups
@@ -365,47 +375,55 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[chunk & 1u]);
       }
-      // the tile's parts meet: token m at [rank][m % TS][row] of CTA m / TS
-      if (S > 1 && alive) {
-        if (tile > 0)
-          alive = __all_sync(0xffffffffu, mbar_wait_cluster(rempty, (tile - 1) & 1u, tmo, abort_flag));
-        if (alive) {
-          for (int c = 0; c < S; ++c) {
-            if (c == rank) continue;
-            const uint32_t dst = mapa_shared(red0 + static_cast<uint32_t>((rank * TS * RM + row) * 4), static_cast<uint32_t>(c));
+      const float bias = (n_ok && a.bias != nullptr) ? static_cast<float>(static_cast<const TY*>(a.bias)[n]) : 0.0f;
+      TY* y = static_cast<TY*>(a.Y) + n;
+      if (S == 1) {
+        if (alive && n_ok) {
 #pragma unroll
-            for (int t = 0; t < C::TH; ++t) {
-              const int k = m0 + t - c * TS;
-              if (k >= 0 && k < TS && m0 + t < M) st_cluster_f32(dst + static_cast<uint32_t>(k * RM * 4), acc[t]);
-            }
+          for (int t = 0; t < C::TH; ++t)
+            if (m0 + t < M) y[static_cast<size_t>(m0 + t) * N] = TY(__fadd_rn(acc[t], bias));
+        }
+      } else {
+        // the tile's parts meet.  The last tile's have been read everywhere:
+        // by the other CTAs (which then also have my copies), and by this one.
+        if (tile > 0 && alive)
+          alive = __all_sync(0xffffffffu, mbar_wait_cluster(rempty, (tile - 1) & 1u, tmo, abort_flag));
+        epi_sync(C::EPI * 32);
+#pragma unroll
+        for (int t = 0; t < C::TH; ++t)
+          if (m0 + t < M) out_s[(m0 + t) * RM + row] = acc[t];
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        epi_sync(C::EPI * 32);
+        if (warp == 4 && lane == 0 && alive && *abort_flag == 0) {
+          if (mine > 0) mbar_arrive_expect_tx(rfull, static_cast<uint32_t>((S - 1) * mine * RM * 4));
+          else mbar_arrive(rfull);
+          for (int c = 0; c < S; ++c) {
+            const int theirs = min(TS, M - c * TS);
+            if (c != rank && theirs > 0)
+              bulk_to_cluster(mapa_shared(smem_u32(red_s + rank * TS * RM), static_cast<uint32_t>(c)),
+                              smem_u32(out_s + c * TS * RM), static_cast<uint32_t>(theirs * RM * 4),
+                              mapa_shared(smem_u32(rfull), static_cast<uint32_t>(c)));
+          }
+        }
+        if (alive) alive = __all_sync(0xffffffffu, mbar_wait_cluster(rfull, tile & 1u, tmo, abort_flag));
+        if (alive) {
+          for (int k = h; k < mine; k += C::NH) {
+            float v = 0.0f;
+            for (int c = 0; c < S; ++c)
+              v = __fadd_rn(v, c == rank ? out_s[(rank * TS + k) * RM + row] : red_s[(c * TS + k) * RM + row]);
+            if (n_ok) y[static_cast<size_t>(rank * TS + k) * N] = TY(__fadd_rn(v, bias));
           }
           __syncwarp();
           if (lane == 0)
             for (int c = 0; c < S; ++c)
-              if (c != rank) mbar_arrive_cluster(mapa_shared(smem_u32(rfull), static_cast<uint32_t>(c)));
-          alive = __all_sync(0xffffffffu, mbar_wait_cluster(rfull, tile & 1u, tmo, abort_flag));
+              if (c != rank) mbar_arrive_cluster(mapa_shared(smem_u32(rempty), static_cast<uint32_t>(c)));
         }
       }
-      if (!alive) {
-        if (lane == 0) rfail(a, abort_flag);
-        break;
-      }
-      const float bias = (n_ok && a.bias != nullptr) ? static_cast<float>(static_cast<const TY*>(a.bias)[n]) : 0.0f;
-#pragma unroll
-      for (int t = 0; t < C::TH; ++t) {
-        const int m = m0 + t, k = m - rank * TS;
-        if (k >= 0 && k < TS && m < M) {
-          float v = 0.0f;
-          for (int c = 0; c < S; ++c) v = __fadd_rn(v, c == rank ? acc[t] : red_s[(c * TS + k) * RM + row]);
-          v = __fadd_rn(v, bias);
-          if (n_ok) static_cast<TY*>(a.Y)[static_cast<size_t>(m) * N + n] = TY(v);
-        }
-      }
-      if (S > 1) {
-        __syncwarp();
-        if (lane == 0)
-          for (int c = 0; c < S; ++c)
-            if (c != rank) mbar_arrive_cluster(mapa_shared(smem_u32(rempty), static_cast<uint32_t>(c)));
+      if (!alive && lane == 0) rfail(a, abort_flag);
+    }
+    if (!alive) {  // copies already issued land before the cluster exits
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
       }
     }
   }
@@ -450,14 +468,14 @@ cudaError_t launch_rows(const CUtensorMap& tmW, const CUtensorMap& tmW16, const 
 
 }  // namespace
 
-int rows_padded_tokens(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+int rows_padded_tokens(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
 
 // Clusters of S CTAs that fit the device at once, one CTA per SM.
 cudaError_t rows_max_clusters(int S, int* clusters) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
-  cudaError_t e = configure_rows<128, __half>(S, cfg, &attr);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(clusters, block_gemm_rows_kernel<128, __half>, &cfg);
+  cudaError_t e = configure_rows<64, __half>(S, cfg, &attr);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(clusters, block_gemm_rows_kernel<64, __half>, &cfg);
   return e;
 }
 
@@ -494,7 +512,6 @@ cudaError_t launch_block_gemm_rows(const CUtensorMap& tmW, const CUtensorMap& tm
     ROWS(16);
     ROWS(32);
     ROWS(64);
-    ROWS(128);
   }
 #undef ROWS
   return cudaErrorInvalidValue;

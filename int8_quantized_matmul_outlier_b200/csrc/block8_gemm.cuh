@@ -17,7 +17,7 @@ cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tm
                                    const BlockGemmArgs& a, int width, int num_sms, cudaStream_t stream);
 
 // Few rows (M <= kRowsMaxM): clusters of `split` CTAs.
-constexpr int64_t kRowsMaxM = 128;
+constexpr int64_t kRowsMaxM = 64;
 struct RowsPlan {
   int split, clusters;
 };
