@@ -344,9 +344,8 @@ void int8mm_free(int8mm_weight_t h);
  * fp16's range becomes Inf.
  *
  * Layouts: activation codes [M, K] row-major; activation scales group-major,
- * sx[g][m] at scales[g * lds + m] with lds >= M a multiple of 4 (the rows of
- * all ceil(K/128) groups are lds long; entries past M are neither read into a
- * result nor written); weight codes [N, K] row-major; weight scales
+ * sx[g][m] at scales[g * lds + m], g < ceil(K/128), with lds >= M a multiple
+ * of 4 (entries past M are neither read nor written); weight codes [N, K] row-major; weight scales
  * [ceil(N/128)][ceil(K/128)].  K and N are multiples of 16, K at most
  * INT8MM_MAX_K; 0 <= M < 2^31, M == 0 is a no-op.  16-bit data is fp16 or
  * bf16 by `dtype`, one type per call.  Pointers are 16-byte aligned.

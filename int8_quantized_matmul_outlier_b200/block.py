@@ -12,7 +12,6 @@ Argument marshalling only, as in the package's other functions.  Work goes to
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import sys
 
@@ -29,48 +28,48 @@ def _groups(k: int) -> int:
     return -(-k // GROUP)
 
 
-class _On:
-    """The device of a call made current, and the raw handle of its stream."""
-
-    __slots__ = ("raw", "_ctx")
-
-    def __init__(self, device: torch.device, stream):
-        self._ctx = None
-        if torch.cuda.current_device() != device.index or stream is not None:
-            self._ctx = contextlib.ExitStack()
-            self._ctx.enter_context(torch.cuda.device(device))
-            if stream is not None:
-                if isinstance(stream, int):
-                    stream = torch.cuda.ExternalStream(stream, device=device)
-                if stream.device != device:
-                    self._ctx.close()
-                    raise ValueError(f"stream on {stream.device}, arguments on {device}")
-                # outputs allocated here belong to the stream that writes them
-                self._ctx.enter_context(torch.cuda.stream(stream))
-
-    def __enter__(self) -> int:
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.close()
+_fn = {}
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
+def _c(name: str):
+    """The C function of that name (looked up once: these calls are short)."""
+    f = _fn.get(name)
+    if f is None:
+        f = _fn[name] = getattr(lib(), name)
+    return f
+
+
+def _here(device: torch.device, stream) -> bool:
+    """Whether a call can run as it stands: on the current device's current stream."""
+    return stream is None and device.index == torch._C._cuda_getDevice()
+
+
+def _raw(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _elsewhere(fn, device: torch.device, stream, *args, **kw):
+    """fn with `device` and `stream` made current: outputs allocated inside
+    belong to the stream that writes them."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, arguments on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+    """Checks a 2-D 16-bit CUDA tensor whose rows are contiguous (any row
+    stride); its type's number."""
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise ValueError(f"{name} must be float16 or bfloat16")
-    return d
-
-
-def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> torch.Tensor:
-    """A 2-D 16-bit CUDA tensor whose rows are contiguous (any row stride)."""
-    if not (t.is_cuda and t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1)):
+    if not (t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)):
         raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
-    _dtype(t, name)
     if like is not None and (t.dtype != like.dtype or t.shape != like.shape or t.device != like.device):
         raise ValueError(f"{name} must have the shape, type and device of its companion")
-    return t
+    return d
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -78,30 +77,28 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _out(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _out(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
 def _new_scales(M: int, G: int, device) -> torch.Tensor:
-    return torch.empty((G, (M + 3) // 4 * 4), dtype=torch.float32, device=device).t()[:M]
+    return torch.empty_strided((M, G), (1, (M + 3) // 4 * 4), dtype=torch.float32, device=device)
 
 
 def _scales_ld(s: torch.Tensor, M: int, G: int, device) -> int:
     """The distance between the groups of scales [M, G]."""
-    if s.dtype != torch.float32 or tuple(s.shape) != (M, G) or s.device != device:
+    if s.dtype != torch.float32 or s.dim() != 2 or s.shape[0] != M or s.shape[1] != G or s.device != device:
         raise ValueError(f"scales must be float32 of shape ({M}, {G}) on {device}")
     if M == 0:
         return 4
-    lds = s.stride(1) if G > 1 else max(s.stride(1), (M + 3) // 4 * 4)
-    if (M > 1 and s.stride(0) != 1) or lds < M or lds % 4 != 0:
+    s0, lds = s.stride()
+    if G == 1 and (lds < M or lds % 4 != 0):
+        lds = (M + 3) // 4 * 4  # no second group to reach
+    if (M > 1 and s0 != 1) or lds < M or lds % 4 != 0:
         raise ValueError("scales must be stored group-major: strides (1, lds), lds >= M a multiple of 4, "
                          "as int8mm_block_quantize returns it")
-    if (s.storage_offset() + (G - 1) * lds + (M + 3) // 4 * 4) * 4 > s.untyped_storage().nbytes():
-        raise ValueError("the storage of scales must hold whole groups (M rounded up to a multiple of 4)")
     return lds
 
 
@@ -123,10 +120,12 @@ def int8mm_block_prepare_weight(W: torch.Tensor, stream=None) -> BlockWeight:
     """Quantise a 16-bit weight W [K, N]; W is not kept."""
     if not (W.is_cuda and W.dim() == 2 and W.is_contiguous()):
         raise ValueError("W must be a contiguous 2-D CUDA tensor")
-    dtype, out = _dtype(W, "W"), _P()
+    dtype = _rows(W, "W")
+    if not _here(W.device, stream):
+        return _elsewhere(int8mm_block_prepare_weight, W.device, stream, W)
+    out = _P()
     K, N = W.shape
-    with _On(W.device, stream) as s:
-        _check(lib().int8mm_block_prepare_weight(W.data_ptr(), dtype, K, N, s, ctypes.byref(out)))
+    _check(_c("int8mm_block_prepare_weight")(W.data_ptr(), dtype, K, N, _raw(W.device), ctypes.byref(out)))
     return BlockWeight(out.value, K, N, W.device)
 
 
@@ -139,31 +138,38 @@ def int8mm_block_prepare_codes(codes: torch.Tensor, scales: torch.Tensor, stream
     if (scales.dtype != torch.float32 or tuple(scales.shape) != (_groups(N), _groups(K))
             or scales.device != codes.device or not scales.is_contiguous()):
         raise ValueError(f"scales must be a contiguous float32 tensor [{_groups(N)}, {_groups(K)}] on codes' device")
+    if not _here(codes.device, stream):
+        return _elsewhere(int8mm_block_prepare_codes, codes.device, stream, codes, scales)
     out = _P()
-    with _On(codes.device, stream) as s:
-        _check(lib().int8mm_block_prepare_codes(codes.data_ptr(), scales.data_ptr(), K, N, s, ctypes.byref(out)))
+    _check(_c("int8mm_block_prepare_codes")(codes.data_ptr(), scales.data_ptr(), K, N, _raw(codes.device),
+                                            ctypes.byref(out)))
     return BlockWeight(out.value, K, N, codes.device)
 
 
 def int8mm_block_weight_codes(w: BlockWeight, stream=None):
     """(codes [N, K] float8_e4m3fn, scales [ceil(N/128), ceil(K/128)] fp32) of a prepared weight."""
-    with _On(w.device, stream) as s:
-        codes = torch.empty((w.N, w.K), dtype=torch.float8_e4m3fn, device=w.device)
-        scales = torch.empty((_groups(w.N), _groups(w.K)), dtype=torch.float32, device=w.device)
-        _check(lib().int8mm_block_weight_codes(w.handle, codes.data_ptr(), scales.data_ptr(), s))
+    if not _here(w.device, stream):
+        return _elsewhere(int8mm_block_weight_codes, w.device, stream, w)
+    codes = torch.empty((w.N, w.K), dtype=torch.float8_e4m3fn, device=w.device)
+    scales = torch.empty((_groups(w.N), _groups(w.K)), dtype=torch.float32, device=w.device)
+    _check(_c("int8mm_block_weight_codes")(w.handle, codes.data_ptr(), scales.data_ptr(), _raw(w.device)))
     return codes, scales
 
 
 def int8mm_block_quantize(X: torch.Tensor, stream=None):
     """(codes [M, K] float8_e4m3fn, scales [M, G]) of 16-bit rows X [M, K]
     (rows contiguous, 16-byte aligned, any row stride)."""
-    _rows(X, "X")
+    dtype, dev = _rows(X, "X"), X.device
+    if not _here(dev, stream):
+        return _elsewhere(int8mm_block_quantize, dev, stream, X)
     M, K = X.shape
-    with _On(X.device, stream) as s:
-        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
-        scales = _new_scales(M, _groups(K), X.device)
-        _check(lib().int8mm_block_quantize(X.data_ptr(), _DTYPES[X.dtype], M, K, _ld(X), codes.data_ptr(),
-                                           scales.data_ptr(), scales.stride(1), s))
+    codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+    lds = (M + 3) // 4 * 4
+    scales = torch.empty_strided((M, _groups(K)), (1, lds), dtype=torch.float32, device=dev)
+    st = _c("int8mm_block_quantize")(X.data_ptr(), dtype, M, K, _ld(X), codes.data_ptr(), scales.data_ptr(), lds,
+                                     _raw(dev))
+    if st:
+        _check(st)
     return codes, scales
 
 
@@ -175,10 +181,10 @@ def int8mm_block_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e
     asked for (``codes=False`` leaves out codes and scales, ``normed`` is the
     16-bit output) or has no residual.  ``residual_out`` may be ``residual`` or
     ``X`` itself, which is then updated in place."""
-    _rows(X, "X")
+    dtype, dev = _rows(X, "X"), X.device
     M, K = X.shape
-    if (not weight.is_cuda or weight.dtype != X.dtype or weight.numel() != K or weight.dim() != 1
-            or not weight.is_contiguous() or weight.device != X.device):
+    if weight.dtype != X.dtype or weight.dim() != 1 or weight.shape[0] != K or weight.device != dev \
+            or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous tensor of K elements of X's type on X's device")
     if residual is not None:
         _rows(residual, "residual", X)
@@ -186,47 +192,54 @@ def int8mm_block_rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e
         raise ValueError("residual_out without a residual")
     if not (codes or normed):
         raise ValueError("neither codes nor the 16-bit output is asked for")
-    with _On(X.device, stream) as s:
-        ro = None if residual is None else _out(residual_out, "residual_out", (M, K), X.dtype, X.device)
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device) if codes else None
-        sc = _new_scales(M, _groups(K), X.device) if codes else None
-        y = torch.empty((M, K), dtype=X.dtype, device=X.device) if normed else None
-        _check(lib().int8mm_block_rms_norm(
-            X.data_ptr(), _ld(X), None if residual is None else residual.data_ptr(),
-            K if residual is None else _ld(residual), weight.data_ptr(), _DTYPES[X.dtype], M, K, float(eps),
-            None if ro is None else ro.data_ptr(), None if y is None else y.data_ptr(),
-            None if q is None else q.data_ptr(), None if sc is None else sc.data_ptr(),
-            (M + 3) // 4 * 4 if sc is None else sc.stride(1), s))
+    if not _here(dev, stream):
+        return _elsewhere(int8mm_block_rms_norm, dev, stream, X, weight, eps, residual, residual_out, codes, normed)
+    ro = q = sc = y = ro_p = q_p = sc_p = y_p = res_p = None
+    ldr, lds = K, (M + 3) // 4 * 4
+    if residual is not None:
+        ro = (torch.empty((M, K), dtype=X.dtype, device=dev) if residual_out is None
+              else _out(residual_out, "residual_out", (M, K), X.dtype, dev))
+        ro_p, res_p, ldr = ro.data_ptr(), residual.data_ptr(), _ld(residual)
+    if codes:
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        sc = torch.empty_strided((M, _groups(K)), (1, lds), dtype=torch.float32, device=dev)
+        q_p, sc_p = q.data_ptr(), sc.data_ptr()
+    if normed:
+        y = torch.empty((M, K), dtype=X.dtype, device=dev)
+        y_p = y.data_ptr()
+    st = _c("int8mm_block_rms_norm")(X.data_ptr(), _ld(X), res_p, ldr, weight.data_ptr(), dtype, M, K, eps, ro_p, y_p,
+                                     q_p, sc_p, lds, _raw(dev))
+    if st:
+        _check(st)
     return q, sc, ro, y
-
-
-def _bias_ptr(bias: torch.Tensor | None, w: BlockWeight, dtype: torch.dtype):
-    if bias is None:
-        return None
-    if bias.dtype != dtype or bias.numel() != w.N or not bias.is_contiguous() or bias.device != w.device:
-        raise ValueError("bias must be a contiguous tensor of N elements of Y's type on the weight's device")
-    return bias.data_ptr()
 
 
 def int8mm_block_matmul(w: BlockWeight, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
                         Y: torch.Tensor | None = None, dtype: torch.dtype = torch.float16, stream=None) -> torch.Tensor:
     """Y [M, N] from activation codes [M, K] and scales [M, G]; ``dtype``
     (float16 or bfloat16) is Y's and the bias's type."""
-    if not (codes.is_cuda and codes.dim() == 2 and codes.is_contiguous() and codes.dtype == torch.float8_e4m3fn):
+    dev = w.device
+    if codes.dtype != torch.float8_e4m3fn or not codes.is_cuda or codes.dim() != 2 or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous 2-D float8_e4m3fn CUDA tensor")
-    M = codes.shape[0]
-    if codes.shape[1] != w.K:
-        raise ValueError(f"codes has {codes.shape[1]} columns, the weight has K={w.K}")
-    if codes.device != w.device:
-        raise ValueError(f"codes on {codes.device}, the weight on {w.device}")
-    if dtype not in _DTYPES:
+    M, K = codes.shape
+    if K != w.K:
+        raise ValueError(f"codes has {K} columns, the weight has K={w.K}")
+    if codes.device != dev:
+        raise ValueError(f"codes on {codes.device}, the weight on {dev}")
+    d = _DTYPES.get(dtype)
+    if d is None:
         raise ValueError("dtype must be float16 or bfloat16")
-    lds = _scales_ld(scales, M, _groups(w.K), codes.device)
-    b = _bias_ptr(bias, w, dtype)
-    with _On(codes.device, stream) as s:
-        Y = _out(Y, "Y", (M, w.N), dtype, codes.device)
-        _check(lib().int8mm_block_matmul(w.handle, codes.data_ptr(), scales.data_ptr(), lds, M, b, Y.data_ptr(),
-                                         _DTYPES[dtype], s))
+    lds = _scales_ld(scales, M, _groups(K), dev)
+    if bias is not None and (bias.dtype != dtype or bias.numel() != w.N or not bias.is_contiguous()
+                             or bias.device != dev):
+        raise ValueError("bias must be a contiguous tensor of N elements of Y's type on the weight's device")
+    if not _here(dev, stream):
+        return _elsewhere(int8mm_block_matmul, dev, stream, w, codes, scales, bias, Y, dtype)
+    Y = torch.empty((M, w.N), dtype=dtype, device=dev) if Y is None else _out(Y, "Y", (M, w.N), dtype, dev)
+    st = _c("int8mm_block_matmul")(w.handle, codes.data_ptr(), scales.data_ptr(), lds, M,
+                                   None if bias is None else bias.data_ptr(), Y.data_ptr(), d, _raw(dev))
+    if st:
+        _check(st)
     return Y
 
 
@@ -239,8 +252,10 @@ def int8mm_block_forward(w: BlockWeight, X: torch.Tensor, bias: torch.Tensor | N
         raise ValueError(f"X has {X.shape[1]} columns, the weight has K={w.K}")
     if X.device != w.device:
         raise ValueError(f"X on {X.device}, the weight on {w.device}")
-    codes, scales = int8mm_block_quantize(X, stream=stream)
-    return int8mm_block_matmul(w, codes, scales, bias=bias, Y=Y, dtype=X.dtype, stream=stream)
+    if not _here(w.device, stream):
+        return _elsewhere(int8mm_block_forward, w.device, stream, w, X, bias, Y)
+    codes, scales = int8mm_block_quantize(X)
+    return int8mm_block_matmul(w, codes, scales, bias, Y, X.dtype)
 
 
 def int8mm_block_get_status(w: BlockWeight) -> int:

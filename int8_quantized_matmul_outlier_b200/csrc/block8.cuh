@@ -42,7 +42,7 @@ struct BlockRowArgs {
   float* scales;         // [G][lds]: group-major, rows lds apart
   int64_t lds;
 };
-cudaError_t launch_block_quantize(const BlockRowArgs& a, int dtype, int num_sms, cudaStream_t stream);
+cudaError_t launch_block_quantize(const BlockRowArgs& a, int dtype, cudaStream_t stream);
 cudaError_t launch_block_rms_norm(const BlockRowArgs& a, int dtype, int num_sms, cudaStream_t stream);
 
 // ---- weights (once per weight) --------------------------------------------
@@ -68,6 +68,7 @@ struct BlockGemmArgs {
   const void* bias;      // [N] of Y's type, or nullptr
   void* Y;               // [M, N]
   int bf16;              // Y's type
+  int tiles, last_rows;  // few rows: the RowsPlan's
   int* status;           // device status word
   unsigned long long timeout_ns;
 };
@@ -76,6 +77,20 @@ struct BlockGemmArgs {
 constexpr int64_t kBlockMaxK = 65536;
 
 #ifdef __CUDACC__
+// Launch attribute that lets a kernel's blocks start while the stream's
+// previous kernel finishes; returns 1, the number of attributes written.  Each
+// kernel of this path calls dependency_wait() in every thread before it
+// touches global memory: what ran before it is then complete, and only its
+// setup overlaps.
+inline unsigned overlap_attribute(cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  return 1;
+}
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------- device helpers
 template <typename T>
 __device__ __forceinline__ float2 pair_to_float(uint32_t w);

@@ -4,8 +4,6 @@
 // into registers and every output written once from there.
 #include "block8.cuh"
 
-#include <algorithm>
-
 namespace i8mm {
 namespace {
 
@@ -25,6 +23,19 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     float_to_pair<T>(v[6], v[7]));
 }
 
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), int64_t blocks, int threads, cudaStream_t stream, const A&... args) {
+  if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap_attribute(&attr);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Maximum over the 16 lanes that hold a group.
 __device__ __forceinline__ uint32_t max16(uint32_t m) {
 #pragma unroll
@@ -33,26 +44,38 @@ __device__ __forceinline__ uint32_t max16(uint32_t m) {
 }
 
 // ------------------------------------------------------------- quantiser
-// 16 lanes per group, 8 values per lane; the groups of all rows are one list.
+// 16 lanes per group, 8 values per lane.  A warp takes a run of VPT * 4 groups
+// of a row, all its loads before the first use: the bytes in flight per SM,
+// not the arithmetic, set the rate.
 constexpr int Q_THREADS = 256;
 
-template <typename T>
-__global__ void __launch_bounds__(Q_THREADS) block_quantize_kernel(const BlockRowArgs a) {
-  const int64_t G = (a.K + kGroup - 1) / kGroup;
-  const int64_t total = a.M * G;
-  const int sub = threadIdx.x & 15;
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (Q_THREADS / 16); u0 < total;
-       u0 += static_cast<int64_t>(gridDim.x) * (Q_THREADS / 16)) {
-    const int64_t u = u0 + (threadIdx.x >> 4);
-    const int64_t row = u / G, g = u - row * G;
-    const int64_t col = g * kGroup + sub * 8;
-    const bool in = u < total && col < a.K;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + row * a.ldx + col), v);
-    float s, r;
+template <typename T, int VPT>
+__global__ void __launch_bounds__(Q_THREADS) block_quantize_kernel(const BlockRowArgs a, unsigned runs) {
+  dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t wid = static_cast<int64_t>(blockIdx.x) * (Q_THREADS / 32) + (threadIdx.x >> 5);
+  const int64_t row = wid / runs;
+  if (row >= a.M) return;
+  const int nvec = static_cast<int>(a.K >> 3);
+  const int c0 = static_cast<int>(wid - row * runs) * (VPT * 32) + lane;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + row * a.ldx);
+  uint4 u[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = c0 + j * 32;
+    u[j] = c < nvec ? __ldg(x + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  uint2* codes = reinterpret_cast<uint2*>(a.codes + row * a.K);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = c0 + j * 32;
+    float v[8], s, r;
+    unpack8<T>(u[j], v);
     group_scale(max16(absmax_bits8(v)), s, r);
-    if (in) *reinterpret_cast<uint2*>(a.codes + row * a.K + col) = e4m3_of8(v, r);
-    if (sub == 0 && u < total) a.scales[g * a.lds + row] = s;
+    if (c < nvec) {
+      codes[c] = e4m3_of8(v, r);
+      if ((lane & 15) == 0) a.scales[static_cast<int64_t>(c >> 4) * a.lds + row] = s;
+    }
   }
 }
 
@@ -68,6 +91,7 @@ template <typename T, int TPR, int VPT, int THREADS>
 __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowArgs a) {
   constexpr int ROWS = THREADS / TPR, WPR = TPR / 32;
   __shared__ float part[THREADS / 32];
+  dependency_wait();
   const int t = threadIdx.x % TPR, rl = threadIdx.x / TPR;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + rl;
   const bool row_ok = row < a.M;
@@ -81,18 +105,27 @@ __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowA
     if (row_ok && c < nvec) h[j] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + row * a.ldx)[c];
   }
   if (a.residual != nullptr) {
+    constexpr int RB = TPR == 1024 && VPT > 4 ? 2 : VPT;  // residual vectors held at a time
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = t + j * TPR;
-      if (row_ok && c < nvec) {
-        const uint4 ru = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + row * a.ldr)[c];
-        float x[8], r[8];
-        unpack8<T>(h[j], x);
-        unpack8<T>(ru, r);
+    for (int j0 = 0; j0 < VPT; j0 += RB) {
+      uint4 ru[RB];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], r[i]);
-        h[j] = pack8<T>(x);
-        reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.K)[c] = h[j];
+      for (int j = 0; j < RB; ++j) {
+        const int c = t + (j0 + j) * TPR;
+        if (row_ok && c < nvec) ru[j] = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + row * a.ldr)[c];
+      }
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        const int c = t + (j0 + j) * TPR;
+        if (row_ok && c < nvec) {
+          float x[8], r[8];
+          unpack8<T>(h[j0 + j], x);
+          unpack8<T>(ru[j], r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], r[i]);
+          h[j0 + j] = pack8<T>(x);
+          reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.K)[c] = h[j0 + j];
+        }
       }
     }
   }
@@ -142,37 +175,60 @@ template <typename T, int TPR, int VPT>
 cudaError_t norm_t(const BlockRowArgs& a, cudaStream_t stream) {
   constexpr int THREADS = TPR < 128 ? 128 : TPR;
   constexpr int ROWS = THREADS / TPR;
-  block_rms_norm_kernel<T, TPR, VPT, THREADS>
-      <<<static_cast<unsigned>((a.M + ROWS - 1) / ROWS), THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(block_rms_norm_kernel<T, TPR, VPT, THREADS>, (a.M + ROWS - 1) / ROWS, THREADS, stream, a);
 }
 
+// Threads per row and vectors per thread.  Few rows: as many threads as the
+// row has vectors, up to 1024, for the shortest chain.  Many rows: 256 threads
+// with up to 8 vectors each, so that several rows per SM are under way and
+// one's loads run under another's sums and stores.
 template <typename T>
-cudaError_t norm_d(const BlockRowArgs& a, cudaStream_t stream) {
+cudaError_t norm_d(const BlockRowArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t nvec = a.K / 8;
   if (nvec <= 32) return norm_t<T, 32, 1>(a, stream);
-  if (nvec <= 128) return norm_t<T, 32, 4>(a, stream);
-  if (nvec <= 512) return norm_t<T, 128, 4>(a, stream);
-  if (nvec <= 1024) return norm_t<T, 256, 4>(a, stream);
-  if (nvec <= 2048) return norm_t<T, 512, 4>(a, stream);
+  if (a.M >= 2 * num_sms) {
+    if (nvec <= 64) return norm_t<T, 32, 2>(a, stream);
+    if (nvec <= 128) return norm_t<T, 32, 4>(a, stream);
+    switch ((nvec + 255) / 256) {
+      case 1: return norm_t<T, 256, 1>(a, stream);
+      case 2: return norm_t<T, 256, 2>(a, stream);
+      case 3: return norm_t<T, 256, 3>(a, stream);
+      case 4: return norm_t<T, 256, 4>(a, stream);
+      case 5: return norm_t<T, 256, 5>(a, stream);
+      case 6: return norm_t<T, 256, 6>(a, stream);
+      case 7: return norm_t<T, 256, 7>(a, stream);
+      case 8: return norm_t<T, 256, 8>(a, stream);
+    }
+  }
+  if (nvec <= 256) return norm_t<T, 256, 1>(a, stream);
+  if (nvec <= 512) return norm_t<T, 512, 1>(a, stream);
+  if (nvec <= 1024) return norm_t<T, 1024, 1>(a, stream);
+  if (nvec <= 2048) return norm_t<T, 1024, 2>(a, stream);
   if (nvec <= 4096) return norm_t<T, 1024, 4>(a, stream);
   return norm_t<T, 1024, 8>(a, stream);
 }
 
+template <typename T>
+cudaError_t quantize_d(const BlockRowArgs& a, cudaStream_t stream) {
+  // runs of 4 vectors per lane; shorter ones for short rows, whose last run
+  // would be mostly empty, and for few rows
+  const int64_t nvec = a.K / 8;
+  const int vpt = a.M * nvec < (1 << 18) ? 1 : (nvec % 128 == 0 || nvec >= 512 ? 4 : (nvec >= 192 ? 2 : 1));
+  const unsigned runs = static_cast<unsigned>((nvec + vpt * 32 - 1) / (vpt * 32));
+  const int64_t blocks = (a.M * runs + Q_THREADS / 32 - 1) / (Q_THREADS / 32);
+  if (vpt == 4) return launch_overlapped(block_quantize_kernel<T, 4>, blocks, Q_THREADS, stream, a, runs);
+  if (vpt == 2) return launch_overlapped(block_quantize_kernel<T, 2>, blocks, Q_THREADS, stream, a, runs);
+  return launch_overlapped(block_quantize_kernel<T, 1>, blocks, Q_THREADS, stream, a, runs);
+}
+
 }  // namespace
 
-cudaError_t launch_block_quantize(const BlockRowArgs& a, int dtype, int num_sms, cudaStream_t stream) {
-  const int64_t units = a.M * block_groups(a.K);
-  const int64_t blocks = (units + Q_THREADS / 16 - 1) / (Q_THREADS / 16);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * 64));
-  if (dtype == kDtypeBf16) block_quantize_kernel<__nv_bfloat16><<<grid, Q_THREADS, 0, stream>>>(a);
-  else block_quantize_kernel<__half><<<grid, Q_THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_block_quantize(const BlockRowArgs& a, int dtype, cudaStream_t stream) {
+  return dtype == kDtypeBf16 ? quantize_d<__nv_bfloat16>(a, stream) : quantize_d<__half>(a, stream);
 }
 
 cudaError_t launch_block_rms_norm(const BlockRowArgs& a, int dtype, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  return dtype == kDtypeBf16 ? norm_d<__nv_bfloat16>(a, stream) : norm_d<__half>(a, stream);
+  return dtype == kDtypeBf16 ? norm_d<__nv_bfloat16>(a, num_sms, stream) : norm_d<__half>(a, num_sms, stream);
 }
 
 }  // namespace i8mm

@@ -28,7 +28,7 @@ struct int8mm_block_weight {
   int64_t K = 0, N = 0, N_pad = 0;
   uint8_t* Wb = nullptr;  // [G][N_pad][128] codes
   float* sw = nullptr;    // [N / 128][G]
-  RowsPlan rows = {1, 1};  // split of products of few rows
+  RowsPlan rows = {1, 1, 1, 16};  // split of products of few rows
   int* status = nullptr;
   unsigned long long timeout_ns = 2000000000ull;
   size_t bytes = 0;
@@ -168,7 +168,9 @@ int8mm_status check_apart(std::initializer_list<Span> outs, std::initializer_lis
 size_t rows_bytes(int64_t M, int64_t K, int64_t ld, size_t elem) {
   return static_cast<size_t>((M - 1) * ld + K) * elem;
 }
-size_t scales_bytes(int64_t K, int64_t lds) { return static_cast<size_t>(block_groups(K) * lds) * 4; }
+size_t scales_bytes(int64_t M, int64_t K, int64_t lds) {
+  return static_cast<size_t>((block_groups(K) - 1) * lds + M) * 4;
+}
 
 void free_all(int8mm_block_weight* h) {
   if (h->Wb) cudaFree(h->Wb);
@@ -273,7 +275,7 @@ int8mm_status int8mm_block_quantize(const void* X_dev, int dtype, int64_t M, int
   if (M == 0) return INT8MM_OK;
   if ((st = check_rows("X", X_dev, ldx, K)) != INT8MM_OK || (st = check_rows("codes", codes_dev, K, K)) != INT8MM_OK ||
       (st = check_scales(scales_dev, lds, M)) != INT8MM_OK ||
-      (st = check_apart({{"codes", codes_dev, static_cast<size_t>(M * K)}, {"scales", scales_dev, scales_bytes(K, lds)}},
+      (st = check_apart({{"codes", codes_dev, static_cast<size_t>(M * K)}, {"scales", scales_dev, scales_bytes(M, K, lds)}},
                         {{"X", X_dev, rows_bytes(M, K, ldx, 2)}})) != INT8MM_OK)
     return st;
   BlockRowArgs a = {};
@@ -284,7 +286,7 @@ int8mm_status int8mm_block_quantize(const void* X_dev, int dtype, int64_t M, int
   a.codes = static_cast<uint8_t*>(codes_dev);
   a.scales = scales_dev;
   a.lds = lds;
-  const cudaError_t e = launch_block_quantize(a, dtype, sm_count(), static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_block_quantize(a, dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "quantiser launch");
 }
 
@@ -315,7 +317,7 @@ int8mm_status int8mm_block_rms_norm(const void* X_dev, int64_t ldx, const void* 
   const Span x = {"X", X_dev, rows_bytes(M, K, ldx, 2)}, w = {"weight", weight_dev, static_cast<size_t>(K) * 2};
   const Span r = {"residual", residual_dev, residual_dev ? rows_bytes(M, K, ldr, 2) : 0};
   const Span c = {"codes", codes_dev, static_cast<size_t>(M * K)};
-  const Span sc = {"scales", scales_dev, codes_dev ? scales_bytes(K, lds) : 0};
+  const Span sc = {"scales", scales_dev, codes_dev ? scales_bytes(M, K, lds) : 0};
   const Span no = {"normed", normed_dev, out2};
   // residual_out may be X or residual in place: each value is read before
   // the same thread writes it
@@ -359,7 +361,7 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
     return fail(INT8MM_ERR_UNSUPPORTED_SHAPE, "M=%lld x N=%lld is too large", (long long)M, (long long)N);
   if ((st = check_apart({{"Y", Y_dev, static_cast<size_t>(M * N) * 2}},
                         {{"codes", codes_dev, static_cast<size_t>(M * K)},
-                         {"scales", scales_dev, scales_bytes(K, lds)},
+                         {"scales", scales_dev, scales_bytes(M, K, lds)},
                          {"bias", bias_dev, static_cast<size_t>(N) * 2}})) != INT8MM_OK)
     return st;
   DeviceGuard dg(h->device);
@@ -385,7 +387,7 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
   const uint32_t box_m = few ? static_cast<uint32_t>(rows_padded_tokens(M)) : 128u;
   const uint64_t G = static_cast<uint64_t>(block_groups(K)), w_rows = G * static_cast<uint64_t>(h->N_pad);
   constexpr CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  CUtensorMap tmX, tmW, tmS, tmW16;
+  CUtensorMap tmX, tmW, tmS, tmWl;
   if ((st = make_tmap(&tmX, u8, codes_dev, static_cast<uint64_t>(K), static_cast<uint64_t>(M),
                       static_cast<uint64_t>(K), kGroup, box_m)) != INT8MM_OK ||
       (st = make_tmap(&tmW, u8, h->Wb, kGroup, w_rows, kGroup, kGroup,
@@ -395,8 +397,12 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
     return st;
   cudaError_t e;
   if (few) {
-    if ((st = make_tmap(&tmW16, u8, h->Wb, kGroup, w_rows, kGroup, kGroup, 16)) != INT8MM_OK) return st;
-    e = launch_block_gemm_rows(tmW, tmW16, tmX, tmS, a, h->rows, s);
+    if ((st = make_tmap(&tmWl, u8, h->Wb, kGroup, w_rows, kGroup, kGroup,
+                        static_cast<uint32_t>(h->rows.last_rows))) != INT8MM_OK)
+      return st;
+    a.tiles = h->rows.tiles;
+    a.last_rows = h->rows.last_rows;
+    e = launch_block_gemm_rows(tmW, tmWl, tmX, tmS, a, h->rows, s);
   } else {
     e = launch_block_gemm_pair(tmX, tmW, tmS, a, width, h->num_sms, s);
   }

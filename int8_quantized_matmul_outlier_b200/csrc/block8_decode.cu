@@ -150,12 +150,13 @@ __device__ __forceinline__ void rows_wait(uint32_t (&r)[N]) {
                  "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])::"memory");
 }
 
-// tmW: the weight's rows of 128 bytes with 128-row boxes; tmW16 with 16-row
-// boxes; tmX: the codes [M, K] with MP-row boxes; tmS: the scales [G][M] with
+// tmW: the weight's rows of 128 bytes with 128-row boxes; tmWl with boxes of
+// a.last_rows, the rows of the longest run's last tile (a shorter run's last
+// tile reads 16 rows too many, and drops them); tmX: the codes [M, K] with MP-row boxes; tmS: the scales [G][M] with
 // 16 x MP boxes.
 template <int MP, typename TY>
 __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
-    block_gemm_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW16,
+    block_gemm_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWl,
                            const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS,
                            const BlockGemmArgs a) {
   using C = RCfg<MP>;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
   uint64_t* tempty = tfull + 2;         // [2]
   uint64_t* sfull = tempty + 2;         // [2]
   uint64_t* sempty = sfull + 2;         // [2]
-  uint64_t* rfull = sempty + 2;         // the other CTAs' parts of my tokens are here
+  uint64_t* rfull = sempty + 2;         // every CTA of the cluster has sent its part of my tokens
   uint64_t* rempty = rfull + 1;         // the other CTAs have read my parts
   uint64_t* drain = rempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
       mbar_init(&sfull[b], 1);
       mbar_init(&sempty[b], C::EPI);
     }
-    mbar_init(rfull, 1);
+    mbar_init(rfull, static_cast<uint32_t>(S));
     mbar_init(rempty, static_cast<uint32_t>(max(1, (S - 1) * C::EPI)));
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const unsigned long long tmo = a.timeout_ns;
+  dependency_wait();
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
@@ -223,7 +225,8 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
     uint32_t phase = 1, chunk = 0;
     bool ok = true;
     for (int r0 = row_begin; r0 < row_end && ok; r0 += RM) {
-      const int rows = min(RM, row_end - r0);
+      const bool last = r0 - row_begin >= (a.tiles - 1) * RM;
+      const int rows = last ? a.last_rows : RM;
       for (int s = 0; s < steps && ok; ++s) {
         const int g = g_begin + s * C::GS, n = min(C::GS, g_end - g);
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, tmo, abort_flag));
@@ -242,11 +245,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
           for (int u = 0; u < n; ++u) {
             uint8_t* w = st + u * C::W_BYTES;
             const int wr = (g + u) * a.N_pad + r0;
-            if (rows == RM) {
-              tma_load_2d_hint(w, &tmW, &full[stage], 0, wr, pol_w);
-            } else {
-              for (int i = 0; i < rows; i += 16) tma_load_2d_hint(w + i * kGroup, &tmW16, &full[stage], 0, wr + i, pol_w);
-            }
+            tma_load_2d_hint(w, last ? &tmWl : &tmW, &full[stage], 0, wr, pol_w);
             tma_load_2d(st + C::GS * C::W_BYTES + u * C::X_BYTES, &tmX, &full[stage], (g + u) * kGroup, 0);
           }
         }
@@ -398,11 +397,16 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
           if (mine > 0) mbar_arrive_expect_tx(rfull, static_cast<uint32_t>((S - 1) * mine * RM * 4));
           else mbar_arrive(rfull);
           for (int c = 0; c < S; ++c) {
+            if (c == rank) continue;
+            const uint32_t bar = mapa_shared(smem_u32(rfull), static_cast<uint32_t>(c));
             const int theirs = min(TS, M - c * TS);
-            if (c != rank && theirs > 0)
+            if (theirs > 0)
               bulk_to_cluster(mapa_shared(smem_u32(red_s + rank * TS * RM), static_cast<uint32_t>(c)),
-                              smem_u32(out_s + c * TS * RM), static_cast<uint32_t>(theirs * RM * 4),
-                              mapa_shared(smem_u32(rfull), static_cast<uint32_t>(c)));
+                              smem_u32(out_s + c * TS * RM), static_cast<uint32_t>(theirs * RM * 4), bar);
+            // also where no token is theirs: a CTA that waited for nobody could
+            // finish a tile before this one has noticed the end of the last,
+            // and rempty would pass two phases unseen
+            mbar_arrive_cluster(bar);
           }
         }
         if (alive) alive = __all_sync(0xffffffffu, mbar_wait_cluster(rfull, tile & 1u, tmo, abort_flag));
@@ -440,7 +444,8 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
 template <int MP, typename TY>
 cudaError_t configure_rows(int S, cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
   auto kern = block_gemm_rows_kernel<MP, TY>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RCfg<MP>::SMEM);
+  static std::atomic<unsigned long long> ready{0};  // one bit per device
+  const cudaError_t e = smem_attribute_once(kern, RCfg<MP>::SMEM, ready);
   if (e != cudaSuccess) return e;
   attr->id = cudaLaunchAttributeClusterDimension;
   attr->val.clusterDim.x = static_cast<unsigned>(S);
@@ -455,15 +460,16 @@ cudaError_t configure_rows(int S, cudaLaunchConfig_t& cfg, cudaLaunchAttribute* 
 }
 
 template <int MP, typename TY>
-cudaError_t launch_rows(const CUtensorMap& tmW, const CUtensorMap& tmW16, const CUtensorMap& tmX,
+cudaError_t launch_rows(const CUtensorMap& tmW, const CUtensorMap& tmWl, const CUtensorMap& tmX,
                         const CUtensorMap& tmS, const BlockGemmArgs& a, const RowsPlan& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  const cudaError_t e = configure_rows<MP, TY>(p.split, cfg, &attr);
+  cudaLaunchAttribute attr[2];
+  const cudaError_t e = configure_rows<MP, TY>(p.split, cfg, attr);
   if (e != cudaSuccess) return e;
+  cfg.numAttrs += overlap_attribute(&attr[cfg.numAttrs]);
   cfg.gridDim = dim3(static_cast<unsigned>(p.split * p.clusters));
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, block_gemm_rows_kernel<MP, TY>, tmW, tmW16, tmX, tmS, a);
+  return cudaLaunchKernelEx(&cfg, block_gemm_rows_kernel<MP, TY>, tmW, tmWl, tmX, tmS, a);
 }
 
 }  // namespace
@@ -484,30 +490,30 @@ cudaError_t rows_max_clusters(int S, int* clusters) {
 // 400 rows' time of one group per tile and CTA of the cluster).
 RowsPlan rows_plan(int64_t N, int64_t K, const int (&max_clusters)[4]) {
   const int64_t units = N / 16, G = block_groups(K);
-  RowsPlan best{1, 1};
+  RowsPlan best{1, 1, 1, 16};
   int64_t best_cost = -1;
   for (int i = 0; i < 4; ++i) {
     const int S = 1 << i;
     if (S > G || max_clusters[i] < 1) continue;
     const int64_t c = std::min<int64_t>(units, max_clusters[i]);
     const int64_t rows = (units + c - 1) / c * 16, groups = (G + S - 1) / S;
-    const int64_t tiles = (rows + RM - 1) / RM;
-    const int64_t cost = std::max<int64_t>(rows, 48) * groups + tiles * (S > 1 ? 400 + 100 * S : 200);
+    const int64_t tiles = (rows + RM - 1) / RM, last = rows - (tiles - 1) * RM;
+    const int64_t cost = ((tiles - 1) * RM + std::max<int64_t>(last, 64)) * groups + tiles * (S > 1 ? 400 + 100 * S : 200);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
-      best = RowsPlan{S, static_cast<int>(c)};
+      best = RowsPlan{S, static_cast<int>(c), static_cast<int>(tiles), static_cast<int>(rows - (tiles - 1) * RM)};
     }
   }
   return best;
 }
 
-cudaError_t launch_block_gemm_rows(const CUtensorMap& tmW, const CUtensorMap& tmW16, const CUtensorMap& tmX,
+cudaError_t launch_block_gemm_rows(const CUtensorMap& tmW, const CUtensorMap& tmWl, const CUtensorMap& tmX,
                                    const CUtensorMap& tmS, const BlockGemmArgs& a, const RowsPlan& p,
                                    cudaStream_t stream) {
 #define ROWS(MP)                                                                              \
   case MP:                                                                                    \
-    return a.bf16 ? launch_rows<MP, __nv_bfloat16>(tmW, tmW16, tmX, tmS, a, p, stream)        \
-                  : launch_rows<MP, __half>(tmW, tmW16, tmX, tmS, a, p, stream)
+    return a.bf16 ? launch_rows<MP, __nv_bfloat16>(tmW, tmWl, tmX, tmS, a, p, stream)        \
+                  : launch_rows<MP, __half>(tmW, tmWl, tmX, tmS, a, p, stream)
   switch (rows_padded_tokens(a.M)) {
     ROWS(16);
     ROWS(32);

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const unsigned long long tmo = a.timeout_ns;
+  dependency_wait();
 
   if (warp < 4) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FRONT));
@@ -459,21 +460,22 @@ template <int BN, typename TY>
 cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS, const BlockGemmArgs& a, int num_sms,
                         cudaStream_t stream) {
   auto kern = block_gemm_pair_kernel<BN, TY>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<BN>::SMEM);
+  static std::atomic<unsigned long long> ready{0};  // one bit per device
+  const cudaError_t e = smem_attribute_once(kern, PCfg<BN>::SMEM, ready);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>((a.M + TILE_M - 1) / TILE_M) * ((a.N + BN - 1) / BN);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, num_sms / 2) * 2));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = PCfg<BN>::SMEM;
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + overlap_attribute(&attr[1]);
   return cudaLaunchKernelEx(&cfg, kern, tmX, tmW, tmS, a);
 }
 

@@ -170,7 +170,6 @@ def test_other_scales_layouts_are_refused():
               torch.zeros(3, 5).t(),                  # groups 5 apart
               torch.zeros(3, 8, dtype=torch.float64).t()[:5],
               torch.zeros(3, 8).t()[:4],              # another M
-              torch.zeros(2, 8).t()[:5],              # another G
-              torch.zeros(3 * 8 - 3).as_strided((5, 3), (1, 8))):  # the last group is cut
+              torch.zeros(2, 8).t()[:5]):             # another G
         with pytest.raises(ValueError):
             block._scales_ld(s, 5, 3, cpu)

@@ -266,6 +266,23 @@ def test_product(M, K, N, dtype):
     assert torch.equal(m.int8mm_block_forward(w, x, bias=bias), yb)
 
 
+@pytest.mark.parametrize("M", [1, 2, 9, 17, 33, 64])
+@pytest.mark.parametrize("K,N", [(8192, 16384), (20480, 5120), (12288, 49152)])
+def test_product_of_few_rows_over_many_tiles(M, K, N):
+    """Runs of several tiles per cluster, tokens fewer than the CTAs that
+    share the sums: the same bits every time, and no wait runs out."""
+    x, w, codes, scales = problem(M, K, N, BF16, M + 1)
+    y = m.int8mm_block_matmul(w, codes, scales, dtype=BF16)
+    wc, ws = m.int8mm_block_weight_codes(w)
+    cols = slice(0, 4096)
+    ref.check_product(y[:, cols], codes, scales, wc[cols], ws[:32], None, K)
+    ref.check_product(y[:, N - 4096:], codes, scales, wc[N - 4096:], ws[-32:], None, K)
+    for _ in range(20):
+        z = m.int8mm_block_matmul(w, codes, scales, dtype=BF16)
+        assert torch.equal(y, z)
+    assert m.int8mm_block_get_status(w) == m.INT8MM_OK
+
+
 def test_product_of_given_codes_of_every_kind():
     """All finite codes, scales over many magnitudes, zero blocks among them."""
     g = gen(11)
