@@ -28,7 +28,7 @@ struct int8mm_block_weight {
   int64_t K = 0, N = 0, N_pad = 0;
   uint8_t* Wb = nullptr;  // [G][N_pad][128] codes
   float* sw = nullptr;    // [N / 128][G]
-  RowsPlan rows = {1, 1, 1, 16};  // split of products of few rows
+  int max_clusters[4] = {};  // of 1, 2, 4 and 8 CTAs, for products of few rows
   int* status = nullptr;
   unsigned long long timeout_ns = 2000000000ull;
   size_t bytes = 0;
@@ -204,9 +204,7 @@ int8mm_status prepare(const void* W, int dtype, const float* scales, int64_t K, 
   h->K = K;
   h->N = N;
   h->N_pad = N_pad;
-  int clusters[4] = {};
-  for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = rows_max_clusters(1 << i, &clusters[i]);
-  h->rows = rows_plan(N, K, clusters);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = rows_max_clusters(1 << i, &h->max_clusters[i]);
   const size_t nsw = static_cast<size_t>((N + kGroup - 1) / kGroup * G);
   const size_t nwb = static_cast<size_t>(G * N_pad) * kGroup;
   if (e == cudaSuccess) e = cudaMallocAsync(reinterpret_cast<void**>(&h->Wb), nwb, s);
@@ -397,12 +395,13 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
     return st;
   cudaError_t e;
   if (few) {
+    const RowsPlan plan = rows_plan(M, N, K, h->max_clusters);
     if ((st = make_tmap(&tmWl, u8, h->Wb, kGroup, w_rows, kGroup, kGroup,
-                        static_cast<uint32_t>(h->rows.last_rows))) != INT8MM_OK)
+                        static_cast<uint32_t>(plan.last_rows))) != INT8MM_OK)
       return st;
-    a.tiles = h->rows.tiles;
-    a.last_rows = h->rows.last_rows;
-    e = launch_block_gemm_rows(tmW, tmWl, tmX, tmS, a, h->rows, s);
+    a.tiles = plan.tiles;
+    a.last_rows = plan.last_rows;
+    e = launch_block_gemm_rows(tmW, tmWl, tmX, tmS, a, plan, s);
   } else {
     e = launch_block_gemm_pair(tmX, tmW, tmS, a, width, h->num_sms, s);
   }

@@ -411,11 +411,26 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
         }
         if (alive) alive = __all_sync(0xffffffffu, mbar_wait_cluster(rfull, tile & 1u, tmo, abort_flag));
         if (alive) {
-          for (int k = h; k < mine; k += C::NH) {
-            float v = 0.0f;
-            for (int c = 0; c < S; ++c)
-              v = __fadd_rn(v, c == rank ? out_s[(rank * TS + k) * RM + row] : red_s[(c * TS + k) * RM + row]);
-            if (n_ok) y[static_cast<size_t>(rank * TS + k) * N] = TY(__fadd_rn(v, bias));
+          // eight tokens at a time: their loads from shared memory, slow while
+          // the next tile's MMAs read it, overlap
+          constexpr int U = C::TH < 8 ? C::TH : 8;
+          for (int k0 = h; k0 < mine; k0 += C::NH * U) {
+            float v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) v[i] = 0.0f;
+            for (int c = 0; c < S; ++c) {
+              const float* part = (c == rank ? out_s + rank * TS * RM : red_s + c * TS * RM) + row;
+#pragma unroll
+              for (int i = 0; i < U; ++i) {
+                const int k = k0 + i * C::NH;
+                if (k < mine) v[i] = __fadd_rn(v[i], part[k * RM]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              const int k = k0 + i * C::NH;
+              if (n_ok && k < mine) y[static_cast<size_t>(rank * TS + k) * N] = TY(__fadd_rn(v[i], bias));
+            }
           }
           __syncwarp();
           if (lane == 0)
@@ -485,10 +500,12 @@ cudaError_t rows_max_clusters(int S, int* clusters) {
   return e;
 }
 
-// Split of K and number of clusters: the least time of the fullest CTA, in
-// rows x groups, plus what a tile costs besides (its sums' meeting, about
-// 400 rows' time of one group per tile and CTA of the cluster).
-RowsPlan rows_plan(int64_t N, int64_t K, const int (&max_clusters)[4]) {
+// Split of K and number of clusters for M tokens: the least time of the
+// fullest CTA, in rows x groups (2.8 ns each at an SM's share of the HBM
+// rate).  A tile of fewer than 64 rows takes the time of 64; the meeting of a
+// tile's sums takes about MEET + MEET_M per token more.
+RowsPlan rows_plan(int64_t M, int64_t N, int64_t K, const int (&max_clusters)[4]) {
+  constexpr int64_t MEET = 500, MEET_M = 20;
   const int64_t units = N / 16, G = block_groups(K);
   RowsPlan best{1, 1, 1, 16};
   int64_t best_cost = -1;
@@ -498,10 +515,10 @@ RowsPlan rows_plan(int64_t N, int64_t K, const int (&max_clusters)[4]) {
     const int64_t c = std::min<int64_t>(units, max_clusters[i]);
     const int64_t rows = (units + c - 1) / c * 16, groups = (G + S - 1) / S;
     const int64_t tiles = (rows + RM - 1) / RM, last = rows - (tiles - 1) * RM;
-    const int64_t cost = ((tiles - 1) * RM + std::max<int64_t>(last, 64)) * groups + tiles * (S > 1 ? 400 + 100 * S : 200);
+    const int64_t cost = ((tiles - 1) * RM + std::max<int64_t>(last, 64)) * groups + tiles * (S > 1 ? MEET + MEET_M * M : 200);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
-      best = RowsPlan{S, static_cast<int>(c), static_cast<int>(tiles), static_cast<int>(rows - (tiles - 1) * RM)};
+      best = RowsPlan{S, static_cast<int>(c), static_cast<int>(tiles), static_cast<int>(last)};
     }
   }
   return best;
