@@ -381,7 +381,7 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
   a.timeout_ns = h->timeout_ns;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool few = M <= kRowsMaxM;
-  const int width = few ? 0 : block_pair_width(M, N, h->num_sms);
+  const int width = few ? 0 : block_pair_width(M, N, K, h->num_sms);
   const uint32_t box_m = few ? static_cast<uint32_t>(rows_padded_tokens(M)) : 128u;
   const uint64_t G = static_cast<uint64_t>(block_groups(K)), w_rows = G * static_cast<uint64_t>(h->N_pad);
   constexpr CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;

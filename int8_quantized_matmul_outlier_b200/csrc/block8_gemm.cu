@@ -13,28 +13,32 @@
 // X and BN / 2 rows of W per group (TMA, 128-byte swizzle, completing on the
 // leader's barrier), keeps its 128 rows of P_g in its own TMEM, sums and
 // writes them.  No multicast.
-//   warps 0, 3  TMA producers, one for X, one for W
+//   warps 0, 3  TMA producers, every second group each
 //   warps 1, 2  in the leader, issue the MMAs of every second group each (4 of
-//               256 x BN x 32), round-robin over the TMEM buffers
+//               256 x 128 x 32 per unit), round-robin over the TMEM buffers
 //   warps 4-11  two per TMEM lane quarter, one row per thread and half of the
 //               tile's columns: they add P_g times sx sw to BN / 2 registers
 //               and write Y at the tile's end, while the next tile's first
 //               two groups already run
-// A group takes the tensor cores 2 BN cycles (BN = 256: 512).  Reading 128 x
-// 256 values from TMEM takes the eight warps 142 cycles, adding them 262 (two
-// per packed instruction), both measured alone, so the sums fit beside the
-// tensor cores; what bounds the kernel is the way of a buffer: its MMAs, the
-// commit, the reads, the arrivals at the leader, the next issue.  A barrier
-// poll takes 200 cycles and more while the MMAs read shared memory, so waits
-// are polled ahead or two at a time, and the reads of the next 32 columns run
-// under the multiply-adds of the last.
-// Units of half a group (N = 128, four buffers) would have more slack, but
-// read the X tile twice from shared memory: 1393 us for 2048 x 12288 x 49152.
 //
-// BN: the tile width is chosen from 256, 192 and 128 so that the tiles fill
-// the pairs' rounds (block_pair_width).  A 192-wide tile does not start on a
-// 128-column block of the weight scales, but its chunks of 32 columns never
-// cross one: a half-tile meets at most two blocks.
+// A group of a 256-wide tile is computed in two units of 128 columns (64 of
+// each CTA's rows of W), so that four TMEM buffers are in turn: from a
+// buffer's MMAs to its next pass the commit, a read, the arrivals of both
+// CTAs at the leader and an issue, each of them a poll or two of barriers,
+// which take 100 to 200 cycles while the MMAs read shared memory.  For the
+// same reason the loads and the MMAs are issued by two warps each, a waiting
+// warp polls its barriers together or ahead of need, and the scales come in
+// boxes of 16 groups.
+//
+// What bounds it: the sums.  Adding 128 x 256 values takes the eight warps 262
+// cycles, and their reads, polls and arrivals as much again (510 ns a group at
+// 2048 x 12288 x 49152; 415 with the multiply-adds left out, of which the
+// loads from L2, 32 KB per SM and group, take 375).  512 cycles, 260 ns, would
+// be the tensor cores' own time.
+//
+// BN: 256, or 128 where that fills the pairs' rounds better (block_pair_width).
+// Widths of 160 and 192, whose halves straddle blocks of the weight scales,
+// took 5% and 18% more per column.
 //
 // Every wait is bounded; a timeout sets the status word and the CTA drains
 // and exits.
@@ -70,17 +74,20 @@ struct PCfg {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 212992 / STAGE;
   static constexpr int HALF = BN / 2;  // columns per epilogue warp
-  static constexpr int BUFS = 512 / BN;  // accumulator buffers in TMEM
-  static constexpr int ISSUERS = 2;  // warps that issue MMAs, group by group in turn
-  static constexpr bool CROSS = HALF != 64 && HALF != 128;  // a half may meet two blocks of the weight scales
-  static constexpr int CW = HALF <= 80 ? HALF : HALF == 96 ? 48 : 32;  // columns per TMEM read
+  // A group of a wide tile is computed in two units of half its columns (half
+  // from each CTA's rows of W), each with a TMEM buffer of its own.
+  static constexpr int UNITS = BN / 128;
+  static constexpr int UNIT = 128;
+  static constexpr int BUFS = 4;
+  static constexpr int ISSUERS = 2;       // warps that issue MMAs, every second group each
+  static constexpr int CW = HALF / UNITS;  // an epilogue warp's columns of a unit
   static constexpr int NBARS = 2 * STAGES + 2 * BUFS + ISSUERS + 4;
   static constexpr int SX_OFF = STAGES * STAGE;
   static constexpr int BAR_OFF = SX_OFF + 2 * SX_CHUNK * BM * 4;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM = MISC_OFF + 16 + 1024;  // + slack to align the base to 1024
-  static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, BN);  // e4m3 and fp16 operands share the encoding 0
-  static_assert(CW % 16 == 0 && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
+  static constexpr uint32_t IDESC = idesc_f16_f32(TILE_M, UNIT);  // e4m3 and fp16 operands share the encoding 0
+  static_assert((BN == 128 || BN == 256) && STAGE % 1024 == 0 && SMEM <= 232448, "tile shape");
 };
 
 // D[tmem of both CTAs] (+)= A * B^T over the pair's shared memory, e4m3 to fp32.
@@ -237,44 +244,49 @@ __global__ void __launch_bounds__(THREADS, 1)
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FRONT));
    if (warp == 0 || warp == 3) {
       // ----------------------------------------------------- TMA producers
-      // Warp 0 loads X and its scales, warp 3 W: issuing both takes one warp
-      // longer than a group's MMAs take the tensor cores.  Both CTAs' loads
-      // complete on the leader's barrier; its warp 0 announces the pair's
-      // bytes.
-      const bool is_x = warp == 0;
+      // Every second group each: its wait and loads take one warp longer than
+      // its MMAs take the tensor cores.  Both CTAs' loads complete on the
+      // leader's barrier; its producer announces the pair's bytes.
+      const int mine = warp == 0 ? 0 : 1;
       const uint32_t issuer = elect_one();
       const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
-      int stage = 0;
-      uint32_t phase = 1, chunk = 0;
+      int stage = mine, g = mine, t = tile0;
+      uint32_t phase = 1, chunk0 = 0;  // chunk0: scale chunks of the tiles before t
+      const uint32_t chunks = static_cast<uint32_t>((G + SX_CHUNK - 1) / SX_CHUNK);
       bool ok = true;
       const uint64_t pol_x = l2_policy_evict_last();  // every column tile of its rows reads X again
-      for (int t = tile0; t < num_tiles && ok; t += tstride) {
+      while (ok) {
+        while (g >= G && t < num_tiles) {
+          g -= G;
+          t += tstride;
+          chunk0 += chunks;
+        }
+        if (t >= num_tiles) break;
         const int m0 = (t % num_m) * TILE_M + static_cast<int>(rank) * BM;
-        int w_row = (t / num_m) * BN + static_cast<int>(rank) * (BN / 2);
-        for (int g = 0; g < G && ok; ++g, w_row += a.N_pad) {
+        const int w0 = (t / num_m) * BN + static_cast<int>(rank) * (BN / 2);
+#pragma unroll 1
+        for (; g < G && ok; g += 2) {
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, tmo, abort_flag));
-          if (ok && is_x && g % SX_CHUNK == 0) {
+          if (ok && g % SX_CHUNK == 0) {
             // the scales of up to 16 groups of this CTA's rows, one box
+            const uint32_t chunk = chunk0 + static_cast<uint32_t>(g / SX_CHUNK);
             ok = __all_sync(0xffffffffu, mbar_wait(&sempty[chunk & 1u], ((chunk >> 1) & 1u) ^ 1u, tmo, abort_flag));
             if (ok && issuer) {
               mbar_arrive_expect_tx(&sfull[chunk & 1u], SX_CHUNK * BM * 4);
               tma_load_2d(sx_s + (chunk & 1u) * (SX_CHUNK * BM), &tmS, &sfull[chunk & 1u], m0, g);
             }
-            ++chunk;
           }
           if (ok && issuer) {
             uint8_t* st = smem + stage * C::STAGE;
             const uint32_t bar = full0 + static_cast<uint32_t>(stage) * 8u;
-            if (is_x) {
-              if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE);
-              tma_load_2d_pair_hint(st, &tmX, bar, g * kGroup, m0, pol_x);
-            } else {
-              tma_load_2d_pair(st + C::A_BYTES, &tmW, bar, 0, w_row);
-            }
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE);
+            tma_load_2d_pair_hint(st, &tmX, bar, g * kGroup, m0, pol_x);
+            tma_load_2d_pair(st + C::A_BYTES, &tmW, bar, 0, g * a.N_pad + w0);
           }
           __syncwarp();
-          if (++stage == C::STAGES) {
-            stage = 0;
+          stage += 2;
+          if (stage >= C::STAGES) {
+            stage -= C::STAGES;
             phase ^= 1u;
           }
         }
@@ -296,27 +308,30 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t issuer = elect_one();
       const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_k_sw128(0) >> 32);
       const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_k_sw128(smem_u32(smem)));
-      int stage = warp - 1, buf = warp - 1;
+      int stage = warp - 1, buf = C::UNITS * (warp - 1);
       uint32_t phase = 0, bphase = 1;
       bool ok = true;
-      int my_tiles = tile0 < num_tiles ? (num_tiles - tile0 + tstride - 1) / tstride : 0;
+      const int my_tiles = tile0 < num_tiles ? (num_tiles - tile0 + tstride - 1) / tstride : 0;
       for (long long it = warp - 1; it < static_cast<long long>(my_tiles) * G && ok; it += C::ISSUERS) {
-        ok = mbar_wait2_warp(&full[stage], phase, &tempty[buf], bphase, tmo, abort_flag);
-        if (ok) {
-          tc_fence_after();
-          if (issuer) {
-            const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
-            const uint32_t bd = ad + (C::A_BYTES >> 4);
-            const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
 #pragma unroll
-            for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
-              mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
-            mma_commit_pair(&tfull[buf], 0x3);
-            mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
+        for (int u = 0; u < C::UNITS; ++u) {
+          ok = ok && mbar_wait2_warp(&full[stage], phase, &tempty[buf + u], bphase, tmo, abort_flag);
+          if (ok) {
+            tc_fence_after();
+            if (issuer) {
+              const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
+              const uint32_t bd = ad + static_cast<uint32_t>((C::A_BYTES + u * C::CW * kGroup) >> 4);
+              const uint32_t d = tmem_base + static_cast<uint32_t>((buf + u) * C::UNIT);
+#pragma unroll
+              for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
+                mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
+              mma_commit_pair(&tfull[buf + u], 0x3);
+              if (u == C::UNITS - 1) mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
-        buf += C::ISSUERS;
+        buf += C::UNITS * C::ISSUERS;
         if (buf >= C::BUFS) {
           buf -= C::BUFS;
           bphase ^= 1u;
@@ -339,9 +354,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ----------------------------------------------------- sums and epilogue
     const int q = warp & 3;             // TMEM lane quarter this warp may read
     const int h = (warp - 4) >> 2;      // half of the tile's columns
-    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::CW);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
-    const int NB = (N + kGroup - 1) / kGroup;
     uint32_t chunk = 0, buf = 0, ph = 0;
     bool alive = true;
     const uint32_t tfull0 = smem_u32(&tfull[0]);
@@ -350,15 +364,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int m = (t % num_m) * TILE_M + static_cast<int>(rank) * BM + q * 32 + lane;
       const int nh = (t / num_m) * BN + h * C::HALF;
       const bool row_ok = m < M;
-      // the weight scales of the one or two blocks that the half-tile meets
-      // (past N: any block's, the sums are dropped), one group per lane, a
-      // chunk ahead
-      const int b0 = min(nh / kGroup, NB - 1), b1 = min((nh + C::HALF - 1) / kGroup, NB - 1);
-      const float* sw0 = a.sw + static_cast<size_t>(b0) * G;
-      const float* sw1 = a.sw + static_cast<size_t>(b1) * G;
-      auto weight_scale = [&](const float* p, int g) { return __ldg(p + min(g + lane, G - 1)); };
-      float w0n = weight_scale(sw0, 0), w1n = weight_scale(sw1, 0);
-      const int cross = (b0 + 1) * kGroup - nh;  // first column of the second block
+      // the weight scales of the half-tile's block (past N: the last block's,
+      // the sums are dropped), one group per lane, a chunk ahead
+      const float* swp = a.sw + static_cast<size_t>(min(nh / kGroup, (N - 1) / kGroup)) * G;
+      auto weight_scale = [&](int g) { return __ldg(swp + min(g + lane, G - 1)); };
+      float wn = weight_scale(0);
       uint64_t acc[C::HALF / 2];
 #pragma unroll
       for (int i = 0; i < C::HALF / 2; ++i) acc[i] = 0ull;
@@ -367,39 +377,33 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ready = false;  // the next group was complete when polled during the last one
 #pragma unroll 1
       for (int g0 = 0; g0 < G && alive; g0 += SX_CHUNK, ++chunk) {
-        const float w0 = w0n, w1 = w1n;
-        w0n = weight_scale(sw0, g0 + SX_CHUNK);
-        w1n = weight_scale(sw1, g0 + SX_CHUNK);
+        const float w = wn;
+        wn = weight_scale(g0 + SX_CHUNK);
         alive = __all_sync(0xffffffffu, mbar_wait(&sfull[chunk & 1u], (chunk >> 1) & 1u, tmo, abort_flag));
         uint32_t sx = sx0 + (chunk & 1u) * (SX_CHUNK * BM * 4);
         const int n = min(SX_CHUNK, G - g0);
 #pragma unroll 1
         for (int j = 0; j < n && alive; ++j, sx += BM * 4) {
-          if (!__all_sync(0xffffffffu, ready)) alive = mbar_wait_poll(tfull0 + buf * 8u, ph, tmo, abort_flag);
-          tc_fence_after();
-          const uint32_t tb = t_row + buf * BN;
-          uint32_t r[C::CW];
-          tmem_ld_cols<C::CW>(tb, r);
           const float x = lds_f32(sx);
-          const uint64_t s0 = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w0, j)));
-          const uint64_t s1 = C::CROSS ? twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w1, j))) : s0;
+          const uint64_t sc = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w, j)));
 #pragma unroll
-          for (int c = 0; c < C::HALF; c += C::CW) {
-            if (c > 0) tmem_ld_cols<C::CW>(tb + c, r);
+          for (int u = 0; u < C::UNITS; ++u) {
+            if (alive && !__all_sync(0xffffffffu, ready)) alive = mbar_wait_poll(tfull0 + buf * 8u, ph, tmo, abort_flag);
+            tc_fence_after();
+            uint32_t r[C::CW];
+            tmem_ld_cols<C::CW>(t_row + buf * C::UNIT, r);
             tmem_wait_cols<C::CW>(r);
-            if (c + C::CW == C::HALF) {  // the buffer is read: hand it back to the leader
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
-              if (++buf == C::BUFS) {
-                buf = 0;
-                ph ^= 1u;
-              }
-              ready = mbar_test_wait(tfull0 + buf * 8u, ph);
+            tc_fence_before();  // the buffer is read: hand it back to the leader
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8u);
+            if (++buf == C::BUFS) {
+              buf = 0;
+              ph ^= 1u;
             }
+            ready = mbar_test_wait(tfull0 + buf * 8u, ph);
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i)
-              fma2(acc[c / 2 + i], r[2 * i], r[2 * i + 1], (C::CROSS && ((c + 2 * i) & ~15) >= cross) ? s1 : s0);
+              fma2(acc[u * C::CW / 2 + i], r[2 * i], r[2 * i + 1], sc);
           }
         }
         __syncwarp();
@@ -481,21 +485,14 @@ cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CU
 
 }  // namespace
 
-// Time of the fullest pair in columns of 256 rows: rounds of tiles x (width
-// + a fixed cost per tile).
-int block_pair_width(int64_t M, int64_t N, int num_sms) {
-  const int64_t pairs = std::max(1, num_sms / 2), num_m = (M + TILE_M - 1) / TILE_M;
-  int best = 0;
-  int64_t best_cost = 0;
-  for (int w : kPairWidths) {
-    const int64_t rounds = (num_m * ((N + w - 1) / w) + pairs - 1) / pairs;
-    const int64_t cost = rounds * (w + 8);
-    if (best == 0 || cost < best_cost) {
-      best = w;
-      best_cost = cost;
-    }
-  }
-  return best;
+// The width whose fullest pair is done first.  A group of a 256-wide tile takes
+// 510 ns and of a 128-wide one 263 (2048 x 12288 x 49152: 1029 and 1060 us), a
+// tile's end about 4 and 2.5 us more.
+int block_pair_width(int64_t M, int64_t N, int64_t K, int num_sms) {
+  const int64_t pairs = std::max(1, num_sms / 2), num_m = (M + TILE_M - 1) / TILE_M, G = block_groups(K);
+  const int64_t wide = (num_m * ((N + 255) / 256) + pairs - 1) / pairs * (510 * G + 4000);
+  const int64_t narrow = (num_m * ((N + 127) / 128) + pairs - 1) / pairs * (263 * G + 2500);
+  return wide <= narrow ? 256 : 128;
 }
 
 cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS, const BlockGemmArgs& a, int width,
@@ -505,8 +502,6 @@ cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tm
     return a.bf16 ? launch_pair<W, __nv_bfloat16>(tmX, tmW, tmS, a, num_sms, stream)    \
                   : launch_pair<W, __half>(tmX, tmW, tmS, a, num_sms, stream)
   PAIR(256);
-  PAIR(192);
-  PAIR(160);
   PAIR(128);
 #undef PAIR
   return cudaErrorInvalidValue;

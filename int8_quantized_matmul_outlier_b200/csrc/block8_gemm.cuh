@@ -23,9 +23,8 @@ cudaError_t smem_attribute_once(F kern, int bytes, std::atomic<unsigned long lon
 // Groups whose scales the kernel loads at a time.
 constexpr int kSxChunk = 16;
 
-// Columns of a tile of the CTA-pair kernel (rows: 256).
-constexpr int kPairWidths[] = {256, 192, 160, 128};
-int block_pair_width(int64_t M, int64_t N, int num_sms);
+// Columns of a tile of the CTA-pair kernel (rows: 256): 256 or 128.
+int block_pair_width(int64_t M, int64_t N, int64_t K, int num_sms);
 // tmX maps the codes [M, K] with 128-row boxes, tmW the weight's rows of 128
 // bytes with width / 2-row boxes, tmS
 // the scales [G][M] with 16 x 128 boxes.
