@@ -350,8 +350,9 @@ void int8mm_free(int8mm_weight_t h);
  * INT8MM_MAX_K; 0 <= M < 2^31, M == 0 is a no-op.  16-bit data is fp16 or
  * bf16 by `dtype`, one type per call.  Pointers are 16-byte aligned.
  *
- * Besides the weight a call uses only the caller's buffers: calls on several
- * streams, threads or captured graphs may share a handle.  Outputs may not
+ * A handle may be used on any stream ordered after its preparation.  Besides
+ * the weight a call uses only the caller's buffers: calls on several streams,
+ * threads or captured graphs may share a handle.  Outputs may not
  * overlap inputs or each other unless the comment says so.  No call
  * allocates except the two prepare calls; none synchronises except
  * int8mm_block_get_status and int8mm_block_free.
@@ -403,6 +404,16 @@ int8mm_status int8mm_block_rms_norm(const void* X_dev, int64_t ldx, const void* 
  * same type, or NULL. */
 int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev, const float* scales_dev, int64_t lds,
                                   int64_t M, const void* bias_dev, void* Y_dev, int dtype, void* stream);
+
+/* Both steps for 16-bit rows X [M, K] (rows ldx elements apart): quantise, then
+ * multiply; Y and bias are of X's type.  The codes and scales in between lie in
+ * `scratch`, 16-byte aligned, of at least the bytes that
+ * int8mm_block_forward_scratch names; what they hold afterwards is unspecified.
+ * The same result as the two calls. */
+int8mm_status int8mm_block_forward(int8mm_block_weight_t h, const void* X_dev, int64_t ldx, int64_t M,
+                                   const void* bias_dev, void* Y_dev, int dtype, void* scratch_dev,
+                                   size_t scratch_bytes, void* stream);
+int8mm_status int8mm_block_forward_scratch(int8mm_block_weight_t h, int64_t M, size_t* bytes);
 
 /* As int8mm_get_status, int8mm_set_wait_limit, int8mm_weight_bytes and
  * int8mm_free, for a block-scaled weight.  A product that timed out leaves

@@ -61,6 +61,8 @@ SIGNATURES = {
     "int8mm_block_rms_norm": (_ST, [_P, _I64, _P, _I64, _P, ctypes.c_int, _I64, _I64, ctypes.c_float,
                                     _P, _P, _P, _P, _I64, _P]),
     "int8mm_block_matmul": (_ST, [_P, _P, _P, _I64, _I64, _P, _P, ctypes.c_int, _P]),
+    "int8mm_block_forward": (_ST, [_P, _P, _I64, _I64, _P, _P, ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "int8mm_block_forward_scratch": (_ST, [_P, _I64, ctypes.POINTER(ctypes.c_size_t)]),
     "int8mm_block_get_status": (_ST, [_P]),
     "int8mm_block_set_wait_limit": (_ST, [_P, ctypes.c_uint64]),
     "int8mm_block_weight_bytes": (_ST, [_P, ctypes.POINTER(ctypes.c_size_t)]),

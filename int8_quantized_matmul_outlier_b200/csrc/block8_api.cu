@@ -169,8 +169,13 @@ size_t rows_bytes(int64_t M, int64_t K, int64_t ld, size_t elem) {
   return static_cast<size_t>((M - 1) * ld + K) * elem;
 }
 size_t scales_bytes(int64_t M, int64_t K, int64_t lds) {
+  if (M == 0) return 0;
   return static_cast<size_t>((block_groups(K) - 1) * lds + M) * 4;
 }
+
+// Layout of a forward's scratch: the codes, then the scales.
+int64_t scales_ld(int64_t M) { return (M + 3) / 4 * 4; }
+size_t codes_room(int64_t M, int64_t K) { return (static_cast<size_t>(M * K) + 255) / 256 * 256; }
 
 void free_all(int8mm_block_weight* h) {
   if (h->Wb) cudaFree(h->Wb);
@@ -406,6 +411,39 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
     e = launch_block_gemm_pair(tmX, tmW, tmS, a, width, h->num_sms, s);
   }
   return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "block-scaled product launch");
+}
+
+int8mm_status int8mm_block_forward_scratch(int8mm_block_weight_t h, int64_t M, size_t* bytes) {
+  if (!live(h) || bytes == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid handle or NULL output");
+  const int8mm_status st = check_m(M);
+  if (st == INT8MM_OK) *bytes = codes_room(M, h->K) + scales_bytes(scales_ld(M), h->K, scales_ld(M));
+  return st;
+}
+
+int8mm_status int8mm_block_forward(int8mm_block_weight_t h, const void* X_dev, int64_t ldx, int64_t M,
+                                   const void* bias_dev, void* Y_dev, int dtype, void* scratch_dev,
+                                   size_t scratch_bytes, void* stream) {
+  size_t need = 0;
+  int8mm_status st = int8mm_block_forward_scratch(h, M, &need);
+  if (st != INT8MM_OK || (st = check_dtype(dtype)) != INT8MM_OK) return st;
+  if (M == 0) return INT8MM_OK;
+  if (scratch_dev == nullptr || scratch_bytes < need)
+    return fail(INT8MM_ERR_INVALID_ARG, "scratch of %zu bytes: need %zu", scratch_dev ? scratch_bytes : 0, need);
+  if (!aligned16(scratch_dev)) return fail(INT8MM_ERR_ALIGNMENT, "scratch must be 16-byte aligned");
+  if ((st = check_rows("X", X_dev, ldx, h->K)) != INT8MM_OK || (st = check_rows("Y", Y_dev, h->N, h->N)) != INT8MM_OK)
+    return st;
+  if (bias_dev != nullptr && !aligned16(bias_dev)) return fail(INT8MM_ERR_ALIGNMENT, "bias must be 16-byte aligned");
+  // Y may lie on neither X nor the scratch; the two steps check the rest
+  if ((st = check_apart({{"Y", Y_dev, static_cast<size_t>(M * h->N) * 2}, {"scratch", scratch_dev, need}},
+                        {{"X", X_dev, rows_bytes(M, h->K, ldx, 2)},
+                         {"bias", bias_dev, static_cast<size_t>(h->N) * 2}})) != INT8MM_OK)
+    return st;
+  DeviceGuard dg(h->device);
+  if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+  float* scales = reinterpret_cast<float*>(static_cast<char*>(scratch_dev) + codes_room(M, h->K));
+  st = int8mm_block_quantize(X_dev, dtype, M, h->K, ldx, scratch_dev, scales, scales_ld(M), stream);
+  return st != INT8MM_OK ? st
+                         : int8mm_block_matmul(h, scratch_dev, scales, scales_ld(M), M, bias_dev, Y_dev, dtype, stream);
 }
 
 int8mm_status int8mm_block_get_status(int8mm_block_weight_t h) {

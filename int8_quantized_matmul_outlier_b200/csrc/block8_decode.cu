@@ -502,10 +502,12 @@ cudaError_t rows_max_clusters(int S, int* clusters) {
 
 // Split of K and number of clusters for M tokens: the least time of the
 // fullest CTA, in rows x groups (2.8 ns each at an SM's share of the HBM
-// rate).  A tile of fewer than 64 rows takes the time of 64; the meeting of a
-// tile's sums takes about MEET + MEET_M per token more.
+// rate).  A tile of fewer than 48 rows takes the time of 48.  The meeting of a
+// tile's sums takes MEET, and where another tile follows, whose MMAs then wait
+// for it, MEET_M per token more: N = K = 8192 takes 24.6 us unsplit and 23.6
+// in pairs with 32 tokens, K = 12288, N = 49152 (six tiles) 100 and 127.
 RowsPlan rows_plan(int64_t M, int64_t N, int64_t K, const int (&max_clusters)[4]) {
-  constexpr int64_t MEET = 500, MEET_M = 20;
+  constexpr int64_t MEET = 700, MEET_M = 40, UNSPLIT = 200;
   const int64_t units = N / 16, G = block_groups(K);
   RowsPlan best{1, 1, 1, 16};
   int64_t best_cost = -1;
@@ -515,7 +517,8 @@ RowsPlan rows_plan(int64_t M, int64_t N, int64_t K, const int (&max_clusters)[4]
     const int64_t c = std::min<int64_t>(units, max_clusters[i]);
     const int64_t rows = (units + c - 1) / c * 16, groups = (G + S - 1) / S;
     const int64_t tiles = (rows + RM - 1) / RM, last = rows - (tiles - 1) * RM;
-    const int64_t cost = ((tiles - 1) * RM + std::max<int64_t>(last, 64)) * groups + tiles * (S > 1 ? MEET + MEET_M * M : 200);
+    const int64_t cost = ((tiles - 1) * RM + std::max<int64_t>(last, 48)) * groups +
+                         (S > 1 ? tiles * MEET + (tiles - 1) * MEET_M * M : tiles * UNSPLIT);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = RowsPlan{S, static_cast<int>(c), static_cast<int>(tiles), static_cast<int>(last)};

@@ -133,6 +133,9 @@ def test_calls_on_an_unknown_handle_are_refused():
     assert L.int8mm_block_matmul(bogus, buf(0), buf(1), 8, 5, None, buf(2), 0, None) == m.INT8MM_ERR_INVALID_ARG
     assert "handle" in m.int8mm_last_error()
     assert L.int8mm_block_weight_codes(bogus, None, None, None) == m.INT8MM_ERR_INVALID_ARG
+    assert L.int8mm_block_forward(bogus, buf(0), 128, 5, None, buf(1), 0, buf(2), 1 << 20, None) == \
+        m.INT8MM_ERR_INVALID_ARG
+    assert L.int8mm_block_forward_scratch(bogus, 5, ctypes.byref(ctypes.c_size_t())) == m.INT8MM_ERR_INVALID_ARG
     assert L.int8mm_block_get_status(bogus) == m.INT8MM_ERR_INVALID_ARG
     assert L.int8mm_block_set_wait_limit(bogus, 10 ** 9) == m.INT8MM_ERR_INVALID_ARG
     n = ctypes.c_size_t()

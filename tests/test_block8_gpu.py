@@ -1,6 +1,8 @@
 """The e4m3 block-scaled operators on the GPU against plain forms: the
 quantisers bit for bit, norms and products against 64 bits within tolerances
 that count roundings (tests/_block8.py)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -363,6 +365,35 @@ def test_quantise_and_norm_write_only_their_outputs():
         body = s[1024:1024 + G * lds].view(G, lds)
         assert torch.equal(body[:, :M].t(), q[1]) and (body[:, M:] == -7).all()
         assert (s[:1024] == -7).all() and (s[1024 + G * lds:] == -7).all()
+
+
+@pytest.mark.parametrize("M", [5, 70, 300])
+def test_forward_keeps_to_its_scratch(M):
+    K, N = 1040, 784
+    x, w, _, _ = problem(M, K, N, F16, 41)
+    want = m.int8mm_block_forward(w, x)
+    L, st = m.lib(), torch.cuda.current_stream().cuda_stream
+    n = ctypes.c_size_t()
+    assert L.int8mm_block_forward_scratch(w.handle, M, ctypes.byref(n)) == 0
+    buf = torch.full((n.value + 8192,), 0x5a, dtype=torch.uint8, device=dev())
+    Y = torch.zeros(M, N, dtype=F16, device=dev())
+
+    def call(scratch=buf.data_ptr() + 4096, size=n.value, y=Y.data_ptr(), dtype=0, ldx=K):
+        return L.int8mm_block_forward(w.handle, x.data_ptr(), ldx, M, None, y, dtype, scratch, size, st)
+
+    assert call(size=n.value - 1) == m.INT8MM_ERR_INVALID_ARG
+    assert call(scratch=None) == m.INT8MM_ERR_INVALID_ARG
+    assert call(scratch=buf.data_ptr() + 4100) == m.INT8MM_ERR_ALIGNMENT
+    assert call(scratch=x.data_ptr()) == m.INT8MM_ERR_INVALID_ARG
+    assert call(y=buf.data_ptr() + 4096) == m.INT8MM_ERR_INVALID_ARG
+    assert call(y=x.data_ptr()) == m.INT8MM_ERR_INVALID_ARG
+    assert call(dtype=3) == m.INT8MM_ERR_INVALID_ARG
+    assert call(ldx=K - 8) == m.INT8MM_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (buf == 0x5a).all() and (Y == 0).all()
+    assert call() == 0
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want) and (buf[:4096] == 0x5a).all() and (buf[4096 + n.value:] == 0x5a).all()
 
 
 # ----------------------------------------------------- streams, graphs, layers
