@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowA
     if (row_ok && c < nvec) h[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(a.X) + row * a.ldx) + c);
   }
   if (a.residual != nullptr) {
+    const uint4* res = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + row * a.ldr);
     constexpr int RB = TPR == 1024 && VPT > 4 ? 2 : VPT;  // residual vectors held at a time
 #pragma unroll
     for (int j0 = 0; j0 < VPT; j0 += RB) {
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowA
 #pragma unroll
       for (int j = 0; j < RB; ++j) {
         const int c = t + (j0 + j) * TPR;
-        if (row_ok && c < nvec) ru[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + row * a.ldr) + c);
+        if (row_ok && c < nvec) ru[j] = __ldcs(res + c);
       }
 #pragma unroll
       for (int j = 0; j < RB; ++j) {

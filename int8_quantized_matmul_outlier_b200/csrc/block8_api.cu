@@ -121,7 +121,8 @@ int8mm_status make_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* 
   const cuuint32_t box[2] = {box_inner, box_rows}, estr[2] = {1, 1};
   const CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? INT8MM_OK
                            : fail(INT8MM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -278,7 +279,8 @@ int8mm_status int8mm_block_quantize(const void* X_dev, int dtype, int64_t M, int
   if (M == 0) return INT8MM_OK;
   if ((st = check_rows("X", X_dev, ldx, K)) != INT8MM_OK || (st = check_rows("codes", codes_dev, K, K)) != INT8MM_OK ||
       (st = check_scales(scales_dev, lds, M)) != INT8MM_OK ||
-      (st = check_apart({{"codes", codes_dev, static_cast<size_t>(M * K)}, {"scales", scales_dev, scales_bytes(M, K, lds)}},
+      (st = check_apart({{"codes", codes_dev, static_cast<size_t>(M * K)},
+                         {"scales", scales_dev, scales_bytes(M, K, lds)}},
                         {{"X", X_dev, rows_bytes(M, K, ldx, 2)}})) != INT8MM_OK)
     return st;
   BlockRowArgs a = {};
@@ -328,8 +330,8 @@ int8mm_status int8mm_block_rms_norm(const void* X_dev, int64_t ldx, const void* 
   const bool on_r = residual_out_dev != nullptr && residual_out_dev == residual_dev && ldr == K;
   const Span none = {"", nullptr, 0};
   if ((st = check_apart({c, sc, no}, {x, r, w})) != INT8MM_OK ||
-      (st = check_apart({{"residual_out", residual_out_dev, out2}}, {on_x ? none : x, on_r ? none : r, w, c, sc, no})) !=
-          INT8MM_OK)
+      (st = check_apart({{"residual_out", residual_out_dev, out2}},
+                        {on_x ? none : x, on_r ? none : r, w, c, sc, no})) != INT8MM_OK)
     return st;
   BlockRowArgs a = {};
   a.X = X_dev;

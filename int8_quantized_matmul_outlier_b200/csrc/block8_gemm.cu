@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   dependency_wait();
 
   if (warp < 4) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FRONT));
-   if (warp == 0 || warp == 3) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_FRONT));
+    if (warp == 0 || warp == 3) {
       // ----------------------------------------------------- TMA producers
       // Every second group each: its wait and loads take one warp longer than
       // its MMAs take the tensor cores.  Both CTAs' loads complete on the
@@ -298,57 +298,57 @@ __global__ void __launch_bounds__(THREADS, 1)
         while (global_timer_ns() - t0 < 200000ull) {
         }
       }
-   } else if (warp <= C::ISSUERS) {
-    if (rank == 0) {
-      // ------------------------------------------------------- MMA issuers
-      // Every ISSUERS-th group: a group's waits and issue take one warp longer
-      // than its MMAs take the tensor cores.  The whole warp walks the loop
-      // and one elected lane issues: the descriptors then stay in uniform
-      // registers.
-      const uint32_t issuer = elect_one();
-      const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_k_sw128(0) >> 32);
-      const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_k_sw128(smem_u32(smem)));
-      int stage = warp - 1, buf = C::UNITS * (warp - 1);
-      uint32_t phase = 0, bphase = 1;
-      bool ok = true;
-      const int my_tiles = tile0 < num_tiles ? (num_tiles - tile0 + tstride - 1) / tstride : 0;
-      for (long long it = warp - 1; it < static_cast<long long>(my_tiles) * G && ok; it += C::ISSUERS) {
+    } else if (warp <= C::ISSUERS) {
+      if (rank == 0) {
+        // ------------------------------------------------------- MMA issuers
+        // Every ISSUERS-th group: a group's waits and issue take one warp longer
+        // than its MMAs take the tensor cores.  The whole warp walks the loop
+        // and one elected lane issues: the descriptors then stay in uniform
+        // registers.
+        const uint32_t issuer = elect_one();
+        const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_k_sw128(0) >> 32);
+        const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_k_sw128(smem_u32(smem)));
+        int stage = warp - 1, buf = C::UNITS * (warp - 1);
+        uint32_t phase = 0, bphase = 1;
+        bool ok = true;
+        const int my_tiles = tile0 < num_tiles ? (num_tiles - tile0 + tstride - 1) / tstride : 0;
+        for (long long it = warp - 1; it < static_cast<long long>(my_tiles) * G && ok; it += C::ISSUERS) {
 #pragma unroll
-        for (int u = 0; u < C::UNITS; ++u) {
-          ok = ok && mbar_wait2_warp(&full[stage], phase, &tempty[buf + u], bphase, tmo, abort_flag);
-          if (ok) {
-            tc_fence_after();
-            if (issuer) {
-              const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
-              const uint32_t bd = ad + static_cast<uint32_t>((C::A_BYTES + u * C::CW * kGroup) >> 4);
-              const uint32_t d = tmem_base + static_cast<uint32_t>((buf + u) * C::UNIT);
+          for (int u = 0; u < C::UNITS; ++u) {
+            ok = ok && mbar_wait2_warp(&full[stage], phase, &tempty[buf + u], bphase, tmo, abort_flag);
+            if (ok) {
+              tc_fence_after();
+              if (issuer) {
+                const uint32_t ad = desc_lo + static_cast<uint32_t>(stage * (C::STAGE >> 4));
+                const uint32_t bd = ad + static_cast<uint32_t>((C::A_BYTES + u * C::CW * kGroup) >> 4);
+                const uint32_t d = tmem_base + static_cast<uint32_t>((buf + u) * C::UNIT);
 #pragma unroll
-              for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
-                mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
-              mma_commit_pair(&tfull[buf + u], 0x3);
-              if (u == C::UNITS - 1) mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
+                for (int kk = 0; kk < kGroup / 32; ++kk)  // 32 bytes along K inside the 128-byte swizzled row
+                  mma_e4m3_pair(d, make_desc(ad + kk * 2, desc_hi), make_desc(bd + kk * 2, desc_hi), C::IDESC, kk != 0);
+                mma_commit_pair(&tfull[buf + u], 0x3);
+                if (u == C::UNITS - 1) mma_commit_pair(&empty[stage], 0x3);  // frees the stage in both CTAs
+              }
+              __syncwarp();
             }
-            __syncwarp();
+          }
+          buf += C::UNITS * C::ISSUERS;
+          if (buf >= C::BUFS) {
+            buf -= C::BUFS;
+            bphase ^= 1u;
+          }
+          stage += C::ISSUERS;
+          if (stage >= C::STAGES) {
+            stage -= C::STAGES;
+            phase ^= 1u;
           }
         }
-        buf += C::UNITS * C::ISSUERS;
-        if (buf >= C::BUFS) {
-          buf -= C::BUFS;
-          bphase ^= 1u;
+        if (!ok && issuer) {
+          gfail(a, abort_flag);
+          mma_commit_pair(&drain[warp - 1], 0x1);
+          mbar_wait(&drain[warp - 1], 0, tmo, nullptr);
         }
-        stage += C::ISSUERS;
-        if (stage >= C::STAGES) {
-          stage -= C::STAGES;
-          phase ^= 1u;
-        }
-      }
-      if (!ok && issuer) {
-        gfail(a, abort_flag);
-        mma_commit_pair(&drain[warp - 1], 0x1);
-        mbar_wait(&drain[warp - 1], 0, tmo, nullptr);
       }
     }
-   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
     // ----------------------------------------------------- sums and epilogue
@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint64_t sc = twice(__fmul_rn(x, __shfl_sync(0xffffffffu, w, j)));
 #pragma unroll
           for (int u = 0; u < C::UNITS; ++u) {
-            if (alive && !__all_sync(0xffffffffu, ready)) alive = mbar_wait_poll(tfull0 + buf * 8u, ph, tmo, abort_flag);
+            if (alive && !__all_sync(0xffffffffu, ready))
+              alive = mbar_wait_poll(tfull0 + buf * 8u, ph, tmo, abort_flag);
             tc_fence_after();
             uint32_t r[C::CW];
             tmem_ld_cols<C::CW>(t_row + buf * C::UNIT, r);
@@ -461,8 +462,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int BN, typename TY>
-cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS, const BlockGemmArgs& a, int num_sms,
-                        cudaStream_t stream) {
+cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS,
+                        const BlockGemmArgs& a, int num_sms, cudaStream_t stream) {
   auto kern = block_gemm_pair_kernel<BN, TY>;
   static std::atomic<unsigned long long> ready{0};  // one bit per device
   const cudaError_t e = smem_attribute_once(kern, PCfg<BN>::SMEM, ready);
@@ -495,8 +496,8 @@ int block_pair_width(int64_t M, int64_t N, int64_t K, int num_sms) {
   return wide <= narrow ? 256 : 128;
 }
 
-cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS, const BlockGemmArgs& a, int width,
-                                   int num_sms, cudaStream_t stream) {
+cudaError_t launch_block_gemm_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CUtensorMap& tmS,
+                                   const BlockGemmArgs& a, int width, int num_sms, cudaStream_t stream) {
 #define PAIR(W)                                                                    \
   if (width == W)                                                                  \
     return a.bf16 ? launch_pair<W, __nv_bfloat16>(tmX, tmW, tmS, a, num_sms, stream)    \

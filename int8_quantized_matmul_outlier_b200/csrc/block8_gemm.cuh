@@ -41,8 +41,9 @@ int rows_padded_tokens(int64_t M);
 cudaError_t rows_max_clusters(int S, int* clusters);
 RowsPlan rows_plan(int64_t M, int64_t N, int64_t K, const int (&max_clusters)[4]);  // for splits of 1, 2, 4, 8
 // tmW and tmWl map the weight's rows of 128 bytes with 128- and
-// p.last_rows-row boxes (a.tiles and a.last_rows are p's), tmX the codes [M, K] with rows_padded_tokens(M)-row boxes, tmS the
-// scales [G][M] with 16 x rows_padded_tokens(M) boxes.
+// p.last_rows-row boxes (a.tiles and a.last_rows are p's), tmX the codes
+// [M, K] with rows_padded_tokens(M)-row boxes, tmS the scales [G][M] with 16 x
+// rows_padded_tokens(M) boxes.
 cudaError_t launch_block_gemm_rows(const CUtensorMap& tmW, const CUtensorMap& tmWl, const CUtensorMap& tmX,
                                    const CUtensorMap& tmS, const BlockGemmArgs& a, const RowsPlan& p,
                                    cudaStream_t stream);

@@ -411,6 +411,46 @@ def test_two_streams_share_a_handle():
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_streams_by_handle_and_in_order():
+    """A stream given as an integer; work queued behind slow work on it."""
+    x, w, codes, scales = problem(40, 1040, 784, F16, 51)
+    want = m.int8mm_block_forward(w, x)
+    st = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device="cuda")
+    late = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):
+            big = big @ big
+            big /= big.norm()
+        late.copy_(x)
+    y = m.int8mm_block_forward(w, late, stream=st.cuda_stream)
+    c, s = m.int8mm_block_quantize(late, stream=st.cuda_stream)
+    z = m.int8mm_block_matmul(w, c, s, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, want)
+
+
+def test_a_weight_is_ready_for_the_work_queued_behind_it():
+    """Preparation, norm and product back to back, with no wait between: each
+    kernel may start while the last one ends, none may read early."""
+    K, N, M = 4096, 4112, 300
+    x = acts(M, K, F16, 1)
+    wt = torch.ones(K, dtype=F16, device=dev())
+    Ws = [(torch.randn(K, N, generator=gen(i), device="cuda") * 0.02).half() for i in range(6)]
+    torch.cuda.synchronize()
+    got = []
+    for W in Ws:
+        w = m.int8mm_block_prepare_weight(W)
+        codes, scales, _, _ = m.int8mm_block_rms_norm(x, wt)
+        got.append((w, codes, scales, m.int8mm_block_matmul(w, codes, scales), m.int8mm_block_forward(w, x[:9])))
+    torch.cuda.synchronize()
+    for w, codes, scales, y, few in got:
+        assert torch.equal(m.int8mm_block_matmul(w, codes, scales), y)
+        assert torch.equal(m.int8mm_block_forward(w, x[:9]), few)
+        ref.check_product(y, codes, scales, *m.int8mm_block_weight_codes(w), None, K)
+
+
 @pytest.mark.parametrize("M", [1, 40, 200, 600])
 def test_captured_runs_replay_side_by_side(M):
     """Two graphs of norm, product, quantise and product over one set of
