@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(Q_THREADS, 6) block_quantize_kernel(const Bloc
 // then residual_out = h, normed = round16(y), codes and scales of y (from
 // fp32, not from its 16-bit rounding).  h is rounded before the norm because
 // it is what the residual stream holds: the norm of residual_out alone gives
-// the same y.  Bound by memory: 2048 x 12288 fp16 with a residual takes 32.4
-// us among others, 5.4 TB/s of its 7 bytes per value; 512 threads per row
-// take the same, registers cut for five blocks per SM 40.  TPR threads hold a row in registers, VPT vectors of 8 values
+// the same y.  Bound by memory: 2048 x 12288 fp16 with a residual takes 31.7
+// us among others, 5.6 TB/s of its 7 bytes per value (33.1 with plain stores of
+// residual_out; 512 threads per row 32.7, 128 threads 40).  TPR threads hold a row in registers, VPT vectors of 8 values
 // each; the sum of squares is fp32, in a fixed order.
 template <typename T, int TPR, int VPT, int THREADS>
 __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowArgs a) {
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowA
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], r[i]);
           h[j0 + j] = pack8<T>(x);
-          reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.K)[c] = h[j0 + j];
+          __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.K) + c, h[j0 + j]);  // read much later
         }
       }
     }

@@ -215,6 +215,15 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const unsigned long long tmo = a.timeout_ns;
+  if (warp == 0 && relect_one()) {
+    // The first tiles of W into L2 while the stream's previous kernel ends: a
+    // hint that needs no order with it.  16 x 8192 x 8192 among others 16.7 ->
+    // 15.2 us, 1 x 12288 x 49152 94.8 -> 91.7.
+    const uint32_t bytes = static_cast<uint32_t>(min(RM, row_end - row_begin) * kGroup);
+    for (int g = g_begin; g < min(g_end, g_begin + C::STAGES * C::GS); ++g)
+      bulk_prefetch_l2(a.Wb + (static_cast<size_t>(g) * a.N_pad + row_begin) * kGroup, bytes);
+  }
+  __syncwarp();
   dependency_wait();
 
   if (warp == 0) {

@@ -238,6 +238,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const unsigned long long tmo = a.timeout_ns;
+  if (warp == 0 && tile0 < num_tiles && elect_one()) {
+    // the first tiles of W into L2 while the stream's previous kernel ends: a
+    // hint that needs no order with it (a tile lies within N_pad)
+    const int row = tile0 / num_m * BN + static_cast<int>(rank) * (BN / 2);
+    for (int g = 0; g < min(G, C::STAGES); ++g)
+      bulk_prefetch_l2(a.Wb + (static_cast<size_t>(g) * a.N_pad + row) * kGroup, C::B_BYTES);
+  }
+  __syncwarp();
   dependency_wait();
 
   if (warp < 4) {

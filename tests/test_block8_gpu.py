@@ -2,6 +2,7 @@
 quantisers bit for bit, norms and products against 64 bits within tolerances
 that count roundings (tests/_block8.py)."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -429,6 +430,60 @@ def test_streams_by_handle_and_in_order():
     z = m.int8mm_block_matmul(w, c, s, stream=st)
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(z, want)
+
+
+def test_host_threads_share_a_handle():
+    x, w, _, _ = problem(33, 1040, 784, F16, 61)
+    xs = [x, x[:1], acts(300, 1040, F16, 62), x[:20]]
+    want = [m.int8mm_block_forward(w, v) for v in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(50):
+                y = m.int8mm_block_forward(w, xs[i])
+                try:
+                    m.int8mm_block_forward(w, xs[i][:, :1024])  # refused, with this thread's message
+                except ValueError:
+                    pass
+            st.synchronize()
+            if not torch.equal(y, want[i]):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 values of X, 2^31 of Y; the last rows are right."""
+    M, K = 66000, 65536
+    x = torch.zeros(M, K, dtype=F16, device=dev())
+    tail = acts(40, K, F16, 71)
+    x[-40:] = tail
+    codes, scales = m.int8mm_block_quantize(x)
+    same_quantised(codes[-40:], scales[-40:], *ref.quantise(tail))
+    assert (scales[:M - 40] == 0).all()
+    del codes, scales
+    wt = torch.ones(K, dtype=F16, device=dev())
+    codes, scales, _, y = m.int8mm_block_rms_norm(x, wt, normed=True)
+    one = m.int8mm_block_rms_norm(tail, wt, normed=True)
+    assert torch.equal(bits(codes[-40:]), bits(one[0])) and torch.equal(scales[-40:], one[1])
+    assert torch.equal(y[-40:], one[3])
+    del x, y, codes, scales
+    torch.cuda.empty_cache()
+    M, K, N = 66000, 144, 32784
+    x, w, codes, scales = problem(M, K, N, BF16, 72)
+    y = m.int8mm_block_matmul(w, codes, scales, dtype=BF16)
+    wc, ws = m.int8mm_block_weight_codes(w)
+    for rows in (slice(0, 3), slice(M // 2, M // 2 + 3), slice(M - 5, M)):
+        ref.check_product(y[rows], codes[rows], scales[rows], wc, ws, None, K)
+    assert m.int8mm_block_get_status(w) == m.INT8MM_OK
 
 
 def test_a_weight_is_ready_for_the_work_queued_behind_it():
