@@ -31,14 +31,16 @@
 // boxes of 16 groups.
 //
 // What bounds it: the sums.  Adding 128 x 256 values takes the eight warps 262
-// cycles, and their reads, polls and arrivals as much again (510 ns a group at
-// 2048 x 12288 x 49152; 415 with the multiply-adds left out, of which the
-// loads from L2, 32 KB per SM and group, take 375).  512 cycles, 260 ns, would
-// be the tensor cores' own time.
+// cycles, and their reads, polls and arrivals as much again.  A group of a
+// 256-wide tile takes 505 ns and of a 128-wide one 235 to 255 (2048 x 12288 x
+// 49152: 1030 us either way, 0.74 of twice the measured bf16 rate; 2048 x 8192
+// x 8192: 133 and 115 us); with the multiply-adds left out 415 and 205.  The
+// tensor cores' own time is 260 and 130.  Under load the power cap takes the
+// clock to 1.43 GHz, and 2048 x 12288 x 49152 to 1220 us.
 //
-// BN: 256, or 128 where that fills the pairs' rounds better (block_pair_width).
-// Widths of 160 and 192, whose halves straddle blocks of the weight scales,
-// took 5% and 18% more per column.
+// BN: 256 or 128, by the pairs' rounds (block_pair_width).  Widths of 160 and
+// 192, whose halves straddle blocks of the weight scales, took 5% and 18% more
+// per column.
 //
 // Every wait is bounded; a timeout sets the status word and the CTA drains
 // and exits.
@@ -495,12 +497,12 @@ cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CU
 }  // namespace
 
 // The width whose fullest pair is done first.  A group of a 256-wide tile takes
-// 510 ns and of a 128-wide one 263 (2048 x 12288 x 49152: 1029 and 1060 us), a
-// tile's end about 4 and 2.5 us more.
+// 505 ns and of a 128-wide one 235 to 255, a tile's end about 4 and 2.5 us more: 2048
+// x 1024 x 4096 takes 18.4 and 20.5 us, 2048 x 20480 x 5120 229 and 188.
 int block_pair_width(int64_t M, int64_t N, int64_t K, int num_sms) {
   const int64_t pairs = std::max(1, num_sms / 2), num_m = (M + TILE_M - 1) / TILE_M, G = block_groups(K);
-  const int64_t wide = (num_m * ((N + 255) / 256) + pairs - 1) / pairs * (510 * G + 4000);
-  const int64_t narrow = (num_m * ((N + 127) / 128) + pairs - 1) / pairs * (263 * G + 2500);
+  const int64_t wide = (num_m * ((N + 255) / 256) + pairs - 1) / pairs * (505 * G + 4000);
+  const int64_t narrow = (num_m * ((N + 127) / 128) + pairs - 1) / pairs * (250 * G + 2500);
   return wide <= narrow ? 256 : 128;
 }
 
