@@ -31,11 +31,12 @@
 // boxes of 16 groups.
 //
 // What bounds it: the sums.  Adding 128 x 256 values takes the eight warps 262
-// cycles, and their reads, polls and arrivals as much again.  A group of a
-// 256-wide tile takes 505 ns and of a 128-wide one 235 to 255 (2048 x 12288 x
-// 49152: 1030 us either way, 0.74 of twice the measured bf16 rate; 2048 x 8192
-// x 8192: 133 and 115 us); with the multiply-adds left out 415 and 205.  The
-// tensor cores' own time is 260 and 130.  Under load the power cap takes the
+// cycles, and their reads, polls and arrivals as much again.  Time over groups,
+// tile ends included, is 480 to 520 ns at 256 columns and 235 to 255 at 128 for
+// K of 8192 and more (2048 x 12288 x 49152: 1030 us either way, 0.74 of twice
+// the measured bf16 rate; 2048 x 8192 x 8192: 133 and 115 us); with the
+// multiply-adds left out 200 to 227 at 128.  The tensor cores' own time is 260
+// and 130.  Under load the power cap takes the
 // clock to 1.43 GHz, and 2048 x 12288 x 49152 to 1220 us.
 //
 // BN: 256 or 128, by the pairs' rounds (block_pair_width).  Widths of 160 and
@@ -496,13 +497,16 @@ cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CU
 
 }  // namespace
 
-// The width whose fullest pair is done first.  A group of a 256-wide tile takes
-// 505 ns and of a 128-wide one 235 to 255, a tile's end about 4 and 2.5 us more: 2048
-// x 1024 x 4096 takes 18.4 and 20.5 us, 2048 x 20480 x 5120 229 and 188.
+// The width whose fullest pair is done first, by a model whose weights (ns a
+// group, ns a tile's end) are chosen so that it names the faster width at the
+// ten shapes timed with both, M 128 to 4096, K 1024 to 20480; its times are
+// within 25% of theirs.  256 and 128: 2048 x 1024 x 4096 takes 18.4 and 20.5
+// us, 1024 x 8192 x 8192 71.7 and 67.6, 2048 x 20480 x 5120 229 and 188; 2048 x
+// 12288 x 49152 takes 1030 either way.
 int block_pair_width(int64_t M, int64_t N, int64_t K, int num_sms) {
   const int64_t pairs = std::max(1, num_sms / 2), num_m = (M + TILE_M - 1) / TILE_M, G = block_groups(K);
   const int64_t wide = (num_m * ((N + 255) / 256) + pairs - 1) / pairs * (505 * G + 4000);
-  const int64_t narrow = (num_m * ((N + 127) / 128) + pairs - 1) / pairs * (250 * G + 2500);
+  const int64_t narrow = (num_m * ((N + 127) / 128) + pairs - 1) / pairs * (240 * G + 2500);
   return wide <= narrow ? 256 : 128;
 }
 
