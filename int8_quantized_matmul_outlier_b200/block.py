@@ -107,12 +107,26 @@ def _scales_ld(s: torch.Tensor, M: int, G: int, device) -> int:
 
 
 class BlockWeight:
-    """A prepared e4m3 weight with block scales (the library-owned handle)."""
+    """A prepared e4m3 weight with block scales (the library-owned handle).
+
+    The weight never changes, so a copy, shallow or deep, is the object itself:
+    the handle has one owner, and int8mm_block_free ends it for every holder.
+    Pickling writes the codes and scales; loading prepares a weight from them."""
 
     def __init__(self, handle: int, K: int, N: int, device: torch.device):
         self.handle = handle
         self.K, self.N = K, N
         self.device = device
+
+    def __copy__(self):
+        return self
+
+    def __deepcopy__(self, memo):
+        return self
+
+    def __reduce__(self):
+        codes, scales = int8mm_block_weight_codes(self)
+        return _from_bytes, (codes.view(torch.uint8), scales)  # plain pickle does not know the 8-bit type
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -148,6 +162,10 @@ def int8mm_block_prepare_codes(codes: torch.Tensor, scales: torch.Tensor, stream
     _check(_c("int8mm_block_prepare_codes")(codes.data_ptr(), scales.data_ptr(), K, N, _raw(codes.device),
                                             ctypes.byref(out)))
     return BlockWeight(out.value, K, N, codes.device)
+
+
+def _from_bytes(codes: torch.Tensor, scales: torch.Tensor) -> BlockWeight:
+    return int8mm_block_prepare_codes(codes.view(torch.float8_e4m3fn), scales)
 
 
 def int8mm_block_weight_codes(w: BlockWeight, stream=None):

@@ -1,0 +1,64 @@
+"""Life of e4m3 weight handles on the GPU: copies, saved and loaded layers,
+freed handles, failed calls, host threads."""
+import copy
+import ctypes
+import gc
+import io
+import pickle
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+import torch
+
+import int8_quantized_matmul_outlier_b200 as m
+from tests import _block8 as ref
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def dev():
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+def normal(*shape, seed, scale=1.0, dtype=F16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def layer(seed, K=272, N=144, dtype=F16, bias=True):
+    w = m.int8mm_block_prepare_weight(normal(K, N, seed=seed, scale=0.02, dtype=dtype))
+    return m.LinearBlock8bit(w, normal(N, seed=seed + 1, dtype=dtype) if bias else None, dtype)
+
+
+# ---------------------------------------------------------------------- copies
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy])
+def test_a_dropped_copy_leaves_the_layer_alone(how):
+    x = normal(5, 272, seed=1)
+    a = layer(2)
+    want = a(x)
+    b = how(a)
+    assert torch.equal(b(x), want)
+    del b
+    gc.collect()
+    other = layer(3)  # takes what the copy may have given back
+    assert torch.equal(a(x), want)
+    del a
+    gc.collect()
+    assert other(x).shape == want.shape and m.int8mm_block_get_status(other._w) == m.INT8MM_OK
+
+
+def test_a_pickled_layer_has_a_weight_of_its_own():
+    x = normal(5, 272, seed=1)
+    a = layer(2)
+    want = a(x)
+    b = pickle.loads(pickle.dumps(a))
+    file = io.BytesIO()
+    torch.save(a, file)
+    file.seek(0)
+    c = torch.load(file, weights_only=False)
+    assert len({a._w.handle, b._w.handle, c._w.handle}) == 3
+    m.int8mm_block_free(a._w)
+    assert torch.equal(b(x), want) and torch.equal(c(x), want)
+    with pytest.raises(m.Int8mmError):
+        pickle.dumps(a)  # freed
