@@ -18,7 +18,7 @@
 #include <mutex>
 #include <new>
 #include <string>
-#include <unordered_set>
+#include <unordered_map>
 
 using namespace i8mm;
 
@@ -36,8 +36,11 @@ struct int8mm_block_weight {
 
 namespace {
 
+// Callers hold a number in place of a pointer.  None is given twice, so a freed
+// handle stays unknown when a later weight takes its memory.
 std::mutex g_mu;
-std::unordered_set<const int8mm_block_weight*> g_live;
+std::unordered_map<uintptr_t, int8mm_block_weight*> g_live;
+uintptr_t g_last_handle = 0;
 
 int8mm_status fail(int8mm_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int8mm_status fail(int8mm_status s, const char* fmt, ...) {
@@ -55,9 +58,10 @@ int8mm_status cuda_fail(cudaError_t e, const char* what) {
               cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool live(const int8mm_block_weight* h) {
+int8mm_block_weight* find(int8mm_block_weight_t handle) {
   std::lock_guard<std::mutex> g(g_mu);
-  return h != nullptr && g_live.count(h) != 0;
+  const auto at = g_live.find(reinterpret_cast<uintptr_t>(handle));
+  return at == g_live.end() ? nullptr : at->second;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -231,11 +235,15 @@ int8mm_status prepare(const void* W, int dtype, const float* scales, int64_t K, 
     free_all(h);
     return cuda_fail(e, "weight preparation");
   }
-  {
+  try {
     std::lock_guard<std::mutex> g(g_mu);
-    g_live.insert(h);
+    g_live.emplace(g_last_handle + 1, h);
+    *out = reinterpret_cast<int8mm_block_weight_t>(++g_last_handle);
+  } catch (const std::bad_alloc&) {
+    cudaStreamSynchronize(s);
+    free_all(h);
+    return fail(INT8MM_ERR_OOM, "host allocation");
   }
-  *out = h;
   return INT8MM_OK;
 }
 
@@ -257,8 +265,10 @@ int8mm_status int8mm_block_prepare_codes(const void* codes_dev, const float* sca
   return prepare(codes_dev, 0, scales_dev, K, N, stream, out);
 }
 
-int8mm_status int8mm_block_weight_codes(int8mm_block_weight_t h, void* codes_dev, float* scales_dev, void* stream) {
-  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+int8mm_status int8mm_block_weight_codes(int8mm_block_weight_t handle, void* codes_dev, float* scales_dev,
+                                        void* stream) {
+  int8mm_block_weight* h = find(handle);
+  if (h == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
   if (codes_dev != nullptr && !aligned16(codes_dev)) return fail(INT8MM_ERR_ALIGNMENT, "codes must be 16-byte aligned");
   DeviceGuard dg(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -351,9 +361,11 @@ int8mm_status int8mm_block_rms_norm(const void* X_dev, int64_t ldx, const void* 
   return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "norm launch");
 }
 
-int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev, const float* scales_dev, int64_t lds,
-                                  int64_t M, const void* bias_dev, void* Y_dev, int dtype, void* stream) {
-  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+int8mm_status int8mm_block_matmul(int8mm_block_weight_t handle, const void* codes_dev, const float* scales_dev,
+                                  int64_t lds, int64_t M, const void* bias_dev, void* Y_dev, int dtype,
+                                  void* stream) {
+  int8mm_block_weight* h = find(handle);
+  if (h == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
   int8mm_status st;
   if ((st = check_dtype(dtype)) != INT8MM_OK || (st = check_m(M)) != INT8MM_OK) return st;
   if (M == 0) return INT8MM_OK;
@@ -415,20 +427,23 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t h, const void* codes_dev
   return e == cudaSuccess ? INT8MM_OK : cuda_fail(e, "block-scaled product launch");
 }
 
-int8mm_status int8mm_block_forward_scratch(int8mm_block_weight_t h, int64_t M, size_t* bytes) {
-  if (!live(h) || bytes == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid handle or NULL output");
+int8mm_status int8mm_block_forward_scratch(int8mm_block_weight_t handle, int64_t M, size_t* bytes) {
+  const int8mm_block_weight* h = find(handle);
+  if (h == nullptr || bytes == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid handle or NULL output");
   const int8mm_status st = check_m(M);
   if (st == INT8MM_OK) *bytes = codes_room(M, h->K) + scales_bytes(scales_ld(M), h->K, scales_ld(M));
   return st;
 }
 
-int8mm_status int8mm_block_forward(int8mm_block_weight_t h, const void* X_dev, int64_t ldx, int64_t M,
+int8mm_status int8mm_block_forward(int8mm_block_weight_t handle, const void* X_dev, int64_t ldx, int64_t M,
                                    const void* bias_dev, void* Y_dev, int dtype, void* scratch_dev,
                                    size_t scratch_bytes, void* stream) {
   size_t need = 0;
-  int8mm_status st = int8mm_block_forward_scratch(h, M, &need);
+  int8mm_status st = int8mm_block_forward_scratch(handle, M, &need);
   if (st != INT8MM_OK || (st = check_dtype(dtype)) != INT8MM_OK) return st;
   if (M == 0) return INT8MM_OK;
+  const int8mm_block_weight* h = find(handle);
+  if (h == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
   if (scratch_dev == nullptr || scratch_bytes < need)
     return fail(INT8MM_ERR_INVALID_ARG, "scratch of %zu bytes: need %zu", scratch_dev ? scratch_bytes : 0, need);
   if (!aligned16(scratch_dev)) return fail(INT8MM_ERR_ALIGNMENT, "scratch must be 16-byte aligned");
@@ -444,12 +459,13 @@ int8mm_status int8mm_block_forward(int8mm_block_weight_t h, const void* X_dev, i
   if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
   float* scales = reinterpret_cast<float*>(static_cast<char*>(scratch_dev) + codes_room(M, h->K));
   st = int8mm_block_quantize(X_dev, dtype, M, h->K, ldx, scratch_dev, scales, scales_ld(M), stream);
-  return st != INT8MM_OK ? st
-                         : int8mm_block_matmul(h, scratch_dev, scales, scales_ld(M), M, bias_dev, Y_dev, dtype, stream);
+  if (st != INT8MM_OK) return st;
+  return int8mm_block_matmul(handle, scratch_dev, scales, scales_ld(M), M, bias_dev, Y_dev, dtype, stream);
 }
 
-int8mm_status int8mm_block_get_status(int8mm_block_weight_t h) {
-  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+int8mm_status int8mm_block_get_status(int8mm_block_weight_t handle) {
+  int8mm_block_weight* h = find(handle);
+  if (h == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
   DeviceGuard dg(h->device);
   cudaError_t e = dg.err;
   int word = 0;
@@ -461,8 +477,9 @@ int8mm_status int8mm_block_get_status(int8mm_block_weight_t h) {
   return (word & kStatusTimeout) ? fail(INT8MM_ERR_TIMEOUT, "a device wait ran out of time") : INT8MM_OK;
 }
 
-int8mm_status int8mm_block_set_wait_limit(int8mm_block_weight_t h, uint64_t timeout_ns) {
-  if (!live(h)) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+int8mm_status int8mm_block_set_wait_limit(int8mm_block_weight_t handle, uint64_t timeout_ns) {
+  int8mm_block_weight* h = find(handle);
+  if (h == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
   if (timeout_ns < 1000000ull)
     return fail(INT8MM_ERR_INVALID_ARG, "timeout %llu ns is below the 1 ms minimum",
                 static_cast<unsigned long long>(timeout_ns));
@@ -470,17 +487,21 @@ int8mm_status int8mm_block_set_wait_limit(int8mm_block_weight_t h, uint64_t time
   return INT8MM_OK;
 }
 
-int8mm_status int8mm_block_weight_bytes(int8mm_block_weight_t h, size_t* bytes) {
-  if (!live(h) || bytes == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid handle or NULL output");
+int8mm_status int8mm_block_weight_bytes(int8mm_block_weight_t handle, size_t* bytes) {
+  const int8mm_block_weight* h = find(handle);
+  if (h == nullptr || bytes == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid handle or NULL output");
   *bytes = h->bytes;
   return INT8MM_OK;
 }
 
-void int8mm_block_free(int8mm_block_weight_t h) {
-  if (h == nullptr) return;
+void int8mm_block_free(int8mm_block_weight_t handle) {
+  int8mm_block_weight* h = nullptr;
   {
     std::lock_guard<std::mutex> g(g_mu);
-    if (g_live.erase(h) == 0) return;
+    const auto at = g_live.find(reinterpret_cast<uintptr_t>(handle));
+    if (at == g_live.end()) return;
+    h = at->second;
+    g_live.erase(at);
   }
   DeviceGuard dg(h->device);
   cudaDeviceSynchronize();

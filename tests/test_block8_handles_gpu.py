@@ -62,3 +62,19 @@ def test_a_pickled_layer_has_a_weight_of_its_own():
     assert torch.equal(b(x), want) and torch.equal(c(x), want)
     with pytest.raises(m.Int8mmError):
         pickle.dumps(a)  # freed
+
+
+# --------------------------------------------------------------- freed handles
+def test_a_freed_handle_stays_unknown():
+    """A weight may lie where a freed one lay; the old handle does not name it."""
+    L, n = m.lib(), ctypes.c_size_t()
+    old = []
+    for seed in range(8):
+        w = layer(seed)._w
+        for h in old:
+            assert h != w.handle
+            assert L.int8mm_block_weight_bytes(h, ctypes.byref(n)) == m.INT8MM_ERR_INVALID_ARG
+            L.int8mm_block_free(h)  # no-op
+        assert L.int8mm_block_weight_bytes(w.handle, ctypes.byref(n)) == m.INT8MM_OK
+        old.append(w.handle)
+        m.int8mm_block_free(w)
