@@ -53,7 +53,10 @@ int8mm_status fail(int8mm_status s, const char* fmt, ...) {
   return s;
 }
 
+// The runtime also keeps a failed call's error for the next one who asks, such
+// as a launch of a later call, or of the caller: it is taken back here.
 int8mm_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
   return fail(e == cudaErrorMemoryAllocation ? INT8MM_ERR_OOM : INT8MM_ERR_CUDA, "%s: %s (%s)", what,
               cudaGetErrorName(e), cudaGetErrorString(e));
 }

@@ -78,3 +78,23 @@ def test_a_freed_handle_stays_unknown():
         assert L.int8mm_block_weight_bytes(w.handle, ctypes.byref(n)) == m.INT8MM_OK
         old.append(w.handle)
         m.int8mm_block_free(w)
+
+
+# ---------------------------------------------------------------- failed calls
+def test_a_failed_preparation_leaves_no_error_behind():
+    """Out of memory once; the next preparation, and the next launch outside
+    the library, are not told of it."""
+    big = torch.zeros(16384, 65536, dtype=F16, device=dev())  # its codes take 1 GB
+    small, x = normal(256, 128, seed=1, scale=0.02), normal(3, 256, seed=2)
+    torch.cuda.synchronize()
+    fill = torch.empty(torch.cuda.mem_get_info()[0] - (600 << 20), dtype=torch.uint8, device=dev())
+    for _ in range(2):
+        with pytest.raises(m.Int8mmError) as e:
+            m.int8mm_block_prepare_weight(big)
+        assert e.value.status == m.INT8MM_ERR_OOM
+    del fill, big
+    torch.cuda.empty_cache()
+    w = m.int8mm_block_prepare_weight(small)
+    y = m.int8mm_block_forward(w, x)
+    codes, scales = m.int8mm_block_quantize(x)
+    ref.check_product(y, codes, scales, *m.int8mm_block_weight_codes(w), None, 256)
