@@ -319,7 +319,9 @@ class LinearBlock8bit(torch.nn.Module):
 
     x is fp16 or bf16 [..., in_features], or a pair (codes, scales) as
     ``RMSNormBlock8bit`` and ``int8mm_block_quantize`` give it (the output is
-    then of ``dtype``).  The 16-bit weight is not kept."""
+    then of ``dtype``).  The 16-bit weight is not kept.  The state dict holds
+    the weight as ``weight_codes`` and ``weight_scales``; loading one prepares
+    a new weight."""
 
     def __init__(self, weight: BlockWeight, bias: torch.Tensor | None = None, dtype: torch.dtype = torch.float16):
         super().__init__()
@@ -337,6 +339,29 @@ class LinearBlock8bit(torch.nn.Module):
             w = int8mm_block_prepare_weight(linear.weight.detach().t().contiguous())
             b = None if linear.bias is None else linear.bias.detach().clone()
         return cls(w, b, linear.weight.dtype)
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        destination[prefix + "weight_codes"], destination[prefix + "weight_scales"] = int8mm_block_weight_codes(self._w)
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys,
+                              error_msgs):
+        names = [prefix + "weight_codes", prefix + "weight_scales"]
+        rest = {k: v for k, v in state_dict.items() if k not in names}
+        super()._load_from_state_dict(rest, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs)
+        missing_keys += [k for k in names if k not in state_dict]
+        if any(k not in state_dict for k in names):
+            return
+        codes, scales = (state_dict[k] for k in names)
+        if codes.dtype != torch.float8_e4m3fn or tuple(codes.shape) != (self.out_features, self.in_features):
+            error_msgs.append(f"{names[0]}: {codes.dtype} {tuple(codes.shape)}, the layer takes torch.float8_e4m3fn "
+                              f"{(self.out_features, self.in_features)}")
+            return
+        try:
+            dev = self._w.device
+            self._w = int8mm_block_prepare_codes(codes.to(dev).contiguous(), scales.to(dev).contiguous())
+        except (ValueError, RuntimeError) as e:
+            error_msgs.append(f"{names[0]}: {e}")
 
     def forward(self, x) -> torch.Tensor:
         if isinstance(x, tuple):

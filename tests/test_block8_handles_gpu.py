@@ -64,6 +64,44 @@ def test_a_pickled_layer_has_a_weight_of_its_own():
         pickle.dumps(a)  # freed
 
 
+# ------------------------------------------------------------------ saved state
+@pytest.mark.parametrize("dtype,bias", [(F16, True), (BF16, False)])
+def test_a_state_dict_holds_the_weight(dtype, bias):
+    x = normal(5, 272, seed=1, dtype=dtype)
+    a, b = (torch.nn.Sequential(torch.nn.Identity(), layer(s, dtype=dtype, bias=bias)) for s in (2, 9))
+    want = a(x)
+    assert not torch.equal(b(x), want)
+    state = a.state_dict()
+    assert set(state) == {"1.weight_codes", "1.weight_scales"} | ({"1.bias"} if bias else set())
+    file = io.BytesIO()
+    torch.save(state, file)
+    file.seek(0)
+    state = torch.load(file, map_location="cpu")
+    b.load_state_dict(state)
+    assert torch.equal(b(x), want)
+    del a
+    gc.collect()
+    assert torch.equal(b(x), want)
+
+
+def test_a_state_dict_that_does_not_fit_is_refused():
+    a, x = layer(2), normal(5, 272, seed=1)
+    want = a(x)
+    good = a.state_dict()
+    with pytest.raises(RuntimeError, match="Missing key.*weight_codes"):
+        a.load_state_dict({"bias": good["bias"]})
+    # (torch loads what fits before it raises: the bias is the layer's own)
+    with pytest.raises(RuntimeError, match="weight_codes"):
+        a.load_state_dict({**layer(3, K=288).state_dict(), "bias": good["bias"]})
+    with pytest.raises(RuntimeError, match="scales"):
+        a.load_state_dict({**good, "weight_scales": good["weight_scales"][:1]})
+    with pytest.raises(RuntimeError, match="Unexpected key.*other"):
+        a.load_state_dict({**good, "other": good["bias"]})
+    assert torch.equal(a(x), want)
+    assert a.load_state_dict({"bias": good["bias"]}, strict=False).missing_keys == ["weight_codes", "weight_scales"]
+    assert torch.equal(a(x), want)
+
+
 # --------------------------------------------------------------- freed handles
 def test_a_freed_handle_stays_unknown():
     """A weight may lie where a freed one lay; the old handle does not name it."""
