@@ -344,11 +344,12 @@ void int8mm_free(int8mm_weight_t h);
  * fp16's range becomes Inf.
  *
  * Layouts: activation codes [M, K] row-major; activation scales group-major,
- * sx[g][m] at scales[g * lds + m], g < ceil(K/128), with lds >= M a multiple
- * of 4 (entries past M are neither read nor written); weight codes [N, K] row-major; weight scales
- * [ceil(N/128)][ceil(K/128)].  K and N are multiples of 16, K at most
- * INT8MM_MAX_K; 0 <= M < 2^31, M == 0 is a no-op.  16-bit data is fp16 or
- * bf16 by `dtype`, one type per call.  Pointers are 16-byte aligned.
+ * sx[g][m] at scales[g * lds + m], g < ceil(K/128), with lds a multiple of 4
+ * from M to 2^32 (entries past M are neither read nor written); weight codes
+ * [N, K] row-major; weight scales [ceil(N/128)][ceil(K/128)].  K and N are
+ * multiples of 16, K at most INT8MM_MAX_K; 0 <= M < 2^31, M == 0 is a no-op.
+ * 16-bit data is fp16 or bf16 by `dtype`, one type per call; its row strides
+ * are below 2^31.  Pointers are 16-byte aligned.
  *
  * A handle may be used on any stream ordered after its preparation.  Besides
  * the weight a call uses only the caller's buffers: calls on several streams,

@@ -145,11 +145,13 @@ int8mm_status check_rows(const char* name, const void* p, int64_t ld, int64_t K)
   return INT8MM_OK;
 }
 
+// (a TMA stride ends at 2^40 bytes)
 int8mm_status check_scales(const float* scales, int64_t lds, int64_t M) {
   if (scales == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "scales is NULL");
-  if (lds < M || lds % 4 != 0 || lds >= (int64_t(1) << 31))
-    return fail(INT8MM_ERR_INVALID_ARG, "scales: stride %lld between groups; need a multiple of 4 that is >= M=%lld",
-                (long long)lds, (long long)M);
+  if (lds < M || lds % 4 != 0 || lds > (int64_t(1) << 32))
+    return fail(INT8MM_ERR_INVALID_ARG,
+                "scales: stride %lld between groups; need a multiple of 4 from M=%lld to 2^32", (long long)lds,
+                (long long)M);
   if (!aligned16(scales)) return fail(INT8MM_ERR_ALIGNMENT, "scales must be 16-byte aligned");
   return INT8MM_OK;
 }
