@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const int tile0 = static_cast<int>(blockIdx.x) / 2;
   const int tstride = static_cast<int>(gridDim.x) / 2;
-  const int num_m = (M + TILE_M - 1) / TILE_M;
-  const int num_tiles = num_m * ((N + BN - 1) / BN);
+  const int num_m = (M - 1) / TILE_M + 1;  // M + TILE_M may pass 2^31
+  const int num_tiles = num_m * ((N - 1) / BN + 1);
   const int G = (a.K + kGroup - 1) / kGroup;
 
   if (threadIdx.x == 0) {
@@ -479,7 +479,7 @@ cudaError_t launch_pair(const CUtensorMap& tmX, const CUtensorMap& tmW, const CU
   static std::atomic<unsigned long long> ready{0};  // one bit per device
   const cudaError_t e = smem_attribute_once(kern, PCfg<BN>::SMEM, ready);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((a.M + TILE_M - 1) / TILE_M) * ((a.N + BN - 1) / BN);
+  const int64_t tiles = static_cast<int64_t>((a.M - 1) / TILE_M + 1) * ((a.N - 1) / BN + 1);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
