@@ -319,7 +319,7 @@ class LinearBlock8bit(torch.nn.Module):
 
     x is fp16 or bf16 [..., in_features], or a pair (codes, scales) as
     ``RMSNormBlock8bit`` and ``int8mm_block_quantize`` give it (the output is
-    then of ``dtype``).  The 16-bit weight is not kept.  The state dict holds
+    then [M, out_features] of ``dtype``).  The 16-bit weight is not kept.  The state dict holds
     the weight as ``weight_codes`` and ``weight_scales``; loading one prepares
     a new weight."""
 
@@ -386,7 +386,9 @@ class RMSNormBlock8bit(torch.nn.Module):
     ``LinearBlock8bit`` takes, for inference.
 
     ``forward(x)`` returns the pair; ``forward(x, residual)`` returns (pair, x +
-    residual)."""
+    residual), with a residual of x's shape.  The pair of an x [..., dim] has
+    one row per vector, codes [M, dim] and scales [M, G], whatever the leading
+    dimensions; the sum keeps x's shape."""
 
     def __init__(self, dim: int, eps: float = 1e-6, dtype: torch.dtype = torch.float16, device=None):
         super().__init__()
@@ -400,6 +402,8 @@ class RMSNormBlock8bit(torch.nn.Module):
         dim = self.weight.numel()
         if x.shape[-1] != dim:
             raise ValueError(f"last dimension {x.shape[-1]} != {dim}")
+        if residual is not None and residual.shape != x.shape:
+            raise ValueError(f"residual of shape {tuple(residual.shape)}, x of {tuple(x.shape)}")
         r = None if residual is None else residual.reshape(-1, dim)
         codes, scales, out, _ = int8mm_block_rms_norm(x.reshape(-1, dim), self.weight.data, self.eps, residual=r)
         return (codes, scales) if residual is None else ((codes, scales), out.reshape(x.shape))
