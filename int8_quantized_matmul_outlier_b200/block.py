@@ -386,9 +386,9 @@ class RMSNormBlock8bit(torch.nn.Module):
     ``LinearBlock8bit`` takes, for inference.
 
     ``forward(x)`` returns the pair; ``forward(x, residual)`` returns (pair, x +
-    residual), with a residual of x's shape.  The pair of an x [..., dim] has
-    one row per vector, codes [M, dim] and scales [M, G], whatever the leading
-    dimensions; the sum keeps x's shape."""
+    residual), with a residual of x's shape or one of the two as rows [M, dim].
+    The pair of an x [..., dim] has one row per vector, codes [M, dim] and
+    scales [M, G], whatever the leading dimensions; the sum keeps x's shape."""
 
     def __init__(self, dim: int, eps: float = 1e-6, dtype: torch.dtype = torch.float16, device=None):
         super().__init__()
@@ -403,7 +403,9 @@ class RMSNormBlock8bit(torch.nn.Module):
         if x.shape[-1] != dim:
             raise ValueError(f"last dimension {x.shape[-1]} != {dim}")
         if residual is not None and residual.shape != x.shape:
-            raise ValueError(f"residual of shape {tuple(residual.shape)}, x of {tuple(x.shape)}")
+            ours, theirs = ([d for d in t.shape[:-1] if d != 1] for t in (x, residual))
+            if ours != theirs and min(len(ours), len(theirs)) > 1:  # rows would meet in storage order
+                raise ValueError(f"residual of shape {tuple(residual.shape)}, x of {tuple(x.shape)}")
         r = None if residual is None else residual.reshape(-1, dim)
         codes, scales, out, _ = int8mm_block_rms_norm(x.reshape(-1, dim), self.weight.data, self.eps, residual=r)
         return (codes, scales) if residual is None else ((codes, scales), out.reshape(x.shape))

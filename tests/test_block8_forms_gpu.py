@@ -38,3 +38,15 @@ def test_the_most_rows():
     assert m.int8mm_block_get_status(w) == m.INT8MM_OK
     del y, codes, scales
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("sx,sr", [((2, 3), (6,)), ((6,), (2, 3)), ((2, 3), (1, 2, 3)), ((1, 6), (6,)), ((), (1,))])
+def test_norm_layer_takes_rows_for_a_batch(sx, sr):
+    """x and the residual of one row order, one of them flattened."""
+    norm = m.RMSNormBlock8bit(272)
+    n = max(torch.Size(sx).numel(), 1)
+    x, r = (torch.randn(n, 272, generator=gen(i), device="cuda").half() for i in (1, 2))
+    want = m.int8mm_block_rms_norm(x, norm.weight.data, norm.eps, residual=r)
+    (codes, scales), out = norm(x.view(*sx, 272), r.view(*sr, 272))
+    assert out.shape == (*sx, 272) and torch.equal(out.view(n, 272), want[2])
+    assert torch.equal(bits(codes), bits(want[0])) and torch.equal(scales, want[1])
