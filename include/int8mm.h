@@ -351,7 +351,9 @@ void int8mm_free(int8mm_weight_t h);
  * 16-bit data is fp16 or bf16 by `dtype`, one type per call; its row strides
  * are below 2^31.  Pointers are 16-byte aligned.
  *
- * A handle may be used on any stream ordered after its preparation.  Besides
+ * A handle may be used on any stream ordered after its preparation.  A weight
+ * is not prepared on a stream that is being captured (INT8MM_ERR_INVALID_ARG),
+ * and lives as long as the graphs that captured its products.  Besides
  * the weight a call uses only the caller's buffers: calls on several streams,
  * threads or captured graphs may share a handle.  Outputs may not
  * overlap inputs or each other unless the comment says so.  No call

@@ -211,9 +211,15 @@ int8mm_status prepare(const void* W, int dtype, const float* scales, int64_t K, 
     return fail(INT8MM_ERR_UNSUPPORTED_SHAPE, "K=%lld x N=%lld exceeds the weight layout's 2^31 rows of 128 bytes",
                 (long long)K, (long long)N);
   if (!aligned16(W)) return fail(INT8MM_ERR_ALIGNMENT, "W must be 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // a captured allocation has no memory before the graph's launch, and new
+  // memory at every launch; the handle would outlive neither
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (const cudaError_t e = cudaStreamIsCapturing(s, &capture); e != cudaSuccess) return cuda_fail(e, "stream query");
+  if (capture != cudaStreamCaptureStatusNone)
+    return fail(INT8MM_ERR_INVALID_ARG, "the stream is being captured: prepare weights before");
   int8mm_block_weight* h = new (std::nothrow) int8mm_block_weight();
   if (h == nullptr) return fail(INT8MM_ERR_OOM, "host allocation");
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaGetDevice(&h->device);
   h->num_sms = sm_count();
   h->K = K;

@@ -136,3 +136,23 @@ def test_a_failed_preparation_leaves_no_error_behind():
     y = m.int8mm_block_forward(w, x)
     codes, scales = m.int8mm_block_quantize(x)
     ref.check_product(y, codes, scales, *m.int8mm_block_weight_codes(w), None, 256)
+
+
+def test_no_preparation_on_a_captured_stream():
+    """Refused, and the capture goes on."""
+    W, x = normal(256, 128, seed=1, scale=0.02), normal(3, 256, seed=2)
+    w = m.int8mm_block_prepare_weight(W)
+    codes, scales = m.int8mm_block_weight_codes(w)
+    want = m.int8mm_block_forward(w, x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = m.int8mm_block_forward(w, x)
+        for prepare in (lambda: m.int8mm_block_prepare_weight(W), lambda: m.int8mm_block_prepare_codes(codes, scales)):
+            with pytest.raises(m.Int8mmError) as e:
+                prepare()
+            assert e.value.status == m.INT8MM_ERR_INVALID_ARG
+        z = m.int8mm_block_forward(w, x[:1])
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, m.int8mm_block_forward(w, x[:1]))
