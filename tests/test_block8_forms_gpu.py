@@ -5,7 +5,8 @@ import torch
 
 import int8_quantized_matmul_outlier_b200 as m
 from tests import _block8 as ref
-from tests.test_block8_gpu import BF16, F16, bits, dev, gen, same_quantised
+from tests._block8_plans import PIPELINES
+from tests.test_block8_gpu import BF16, F16, acts, bits, dev, gen, problem, same_quantised
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,46 @@ def test_norm_layer_takes_rows_for_a_batch(sx, sr):
     (codes, scales), out = norm(x.view(*sx, 272), r.view(*sr, 272))
     assert out.shape == (*sx, 272) and torch.equal(out.view(n, 272), want[2])
     assert torch.equal(bits(codes), bits(want[0])) and torch.equal(scales, want[1])
+
+
+# ------------------------------------------------------- every form of the kernels
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("M,K", [(2100, 1024), (1400, 2064), (2000, 1552), (600, 5136), (300, 12288)])
+def test_quantise_runs_of_several_vectors(M, K, dtype, wide):
+    """2 and 4 vectors per lane, with a full and a ragged last run."""
+    x = acts(M, K, dtype, M + K, wide)
+    codes, scales = m.int8mm_block_quantize(x)
+    same_quantised(codes, scales, *ref.quantise(x))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("with_residual", [False, True])
+@pytest.mark.parametrize("M,K", [
+    (300, 272), (297, 512), (299, 528), (300, 1024),                          # a warp per row
+    (300, 1040), (300, 2064), (300, 4112), (300, 6160), (300, 8192), (300, 9216), (300, 12288), (300, 13328),
+    (300, 16384),                                                             # 256 threads, 1 to 8 vectors each
+    (300, 16400), (300, 32784),                                               # many rows past those
+    (1, 2064), (9, 4096), (1, 4112), (9, 8192), (295, 8176), (9, 16384), (9, 32768)])  # few rows
+def test_norm_threads_and_vectors(M, K, dtype, with_residual):
+    x = acts(M, K, dtype, M + K)
+    r = acts(M, K, dtype, M + K + 1) if with_residual else None
+    wt = (1 + 0.3 * torch.randn(K, generator=gen(K), device="cuda")).to(dtype)
+    codes, scales, ro, y = m.int8mm_block_rms_norm(x, wt, 1e-5, residual=r, normed=True)
+    h, y64 = ref.norm(x, r, wt, 1e-5)
+    assert ro is None if r is None else torch.equal(ro, h)
+    ref.check_normed(y, y64)
+    ref.check_quantised(codes, scales, y64)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("M,K,N", [p[:3] for p in PIPELINES])
+def test_product_over_several_tiles_and_boxes_of_scales(M, K, N, dtype):
+    x, w, codes, scales = problem(M, K, N, dtype, M + K + N)
+    bias = (torch.randn(N, generator=gen(7), device="cuda") * 0.5).to(dtype)
+    y = m.int8mm_block_matmul(w, codes, scales, bias=bias, dtype=dtype)
+    ref.check_product(y, codes, scales, *m.int8mm_block_weight_codes(w), bias, K)
+    for _ in range(5):
+        assert torch.equal(m.int8mm_block_matmul(w, codes, scales, bias=bias, dtype=dtype), y)
+    assert torch.equal(m.int8mm_block_forward(w, x, bias=bias), y)
+    assert m.int8mm_block_get_status(w) == m.INT8MM_OK

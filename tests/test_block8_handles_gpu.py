@@ -5,6 +5,8 @@ import ctypes
 import gc
 import io
 import pickle
+import threading
+import time
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -156,3 +158,38 @@ def test_no_preparation_on_a_captured_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(z, m.int8mm_block_forward(w, x[:1]))
+
+
+# ---------------------------------------------------------------- host threads
+def test_host_threads_have_their_own_errors():
+    """Products of one handle on a stream per thread, between calls that the
+    library refuses; each thread reads its own message.  What fails in a thread
+    fails the test."""
+    K, N = 1040, 784
+    w = m.int8mm_block_prepare_weight(normal(K, N, seed=1, scale=0.02))
+    xs = [normal(M, K, seed=M) for M in (33, 1, 300, 20)]
+    want = [m.int8mm_block_forward(w, x) for x in xs]
+    torch.cuda.synchronize()
+    L, start = m.lib(), threading.Barrier(len(xs))
+
+    def work(i):
+        st, ld = torch.cuda.Stream(), K - 8 * (i + 1)
+        start.wait(timeout=60)
+        for _ in range(100):
+            y = m.int8mm_block_forward(w, xs[i], stream=st)
+            assert L.int8mm_block_quantize(xs[i].data_ptr(), 0, xs[i].shape[0], K, ld, None, None, 4, None) == \
+                m.INT8MM_ERR_INVALID_ARG
+            time.sleep(0)  # another thread's turn
+            assert f"row stride {ld} " in m.int8mm_last_error()
+        st.synchronize()
+        return torch.equal(y, want[i])
+
+    with ThreadPoolExecutor(len(xs)) as pool:
+        jobs = [pool.submit(work, i) for i in range(len(xs))]
+        assert all(j.result(timeout=120) for j in jobs)
+
+
+def test_the_default_stream_by_its_number():
+    x, l = normal(5, 272, seed=1), layer(2, bias=False)
+    want = l(x)
+    assert torch.equal(m.int8mm_block_forward(l._w, x, stream=torch.cuda.default_stream().cuda_stream), want)
