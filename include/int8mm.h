@@ -426,6 +426,20 @@ int8mm_status int8mm_block_set_wait_limit(int8mm_block_weight_t h, uint64_t time
 int8mm_status int8mm_block_weight_bytes(int8mm_block_weight_t h, size_t* bytes);
 void int8mm_block_free(int8mm_block_weight_t h);
 
+/* As int8mm_set_test_skip: failure-detection tests only, off by default.  Later
+ * products of this handle leave out the arrivals that `bits` names, and change
+ * nothing else (no address, load or store), so that device waits run out:
+ *   INT8MM_BLOCK_TEST_SKIP_SCALES   one summing warp per cluster does not hand
+ *                                   back its boxes of scales; the wait is that
+ *                                   of a CTA for its third box;
+ *   INT8MM_BLOCK_TEST_SKIP_MEETING  M <= 64 with K split over a cluster: its
+ *                                   CTA 0 does not count itself where the
+ *                                   others' partial sums meet.
+ * INT8MM_ERR_INVALID_ARG for other bits. */
+#define INT8MM_BLOCK_TEST_SKIP_SCALES 1
+#define INT8MM_BLOCK_TEST_SKIP_MEETING 2
+int8mm_status int8mm_block_set_test_skip(int8mm_block_weight_t h, int bits);
+
 /* Message of the last error returned on this host thread ("" if none). */
 const char* int8mm_last_error(void);
 

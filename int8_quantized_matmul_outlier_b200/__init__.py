@@ -65,6 +65,7 @@ SIGNATURES = {
     "int8mm_block_forward_scratch": (_ST, [_P, _I64, ctypes.POINTER(ctypes.c_size_t)]),
     "int8mm_block_get_status": (_ST, [_P]),
     "int8mm_block_set_wait_limit": (_ST, [_P, ctypes.c_uint64]),
+    "int8mm_block_set_test_skip": (_ST, [_P, ctypes.c_int]),
     "int8mm_block_weight_bytes": (_ST, [_P, ctypes.POINTER(ctypes.c_size_t)]),
     "int8mm_block_free": (None, [_P]),
 }
@@ -330,7 +331,7 @@ def int8mm_free(w: Weight) -> None:
 
 from .linear import Linear8bitLt  # noqa: E402  (the layer over the functions above)
 from .block import (  # noqa: E402  (the e4m3 block-scaled path)
-    BlockWeight, LinearBlock8bit, RMSNormBlock8bit, int8mm_block_forward, int8mm_block_free,
-    int8mm_block_get_status, int8mm_block_matmul, int8mm_block_prepare_codes, int8mm_block_prepare_weight,
-    int8mm_block_quantize, int8mm_block_rms_norm, int8mm_block_set_wait_limit, int8mm_block_weight_bytes,
-    int8mm_block_weight_codes)
+    INT8MM_BLOCK_TEST_SKIP_MEETING, INT8MM_BLOCK_TEST_SKIP_SCALES, BlockWeight, LinearBlock8bit, RMSNormBlock8bit,
+    int8mm_block_forward, int8mm_block_free, int8mm_block_get_status, int8mm_block_matmul,
+    int8mm_block_prepare_codes, int8mm_block_prepare_weight, int8mm_block_quantize, int8mm_block_rms_norm,
+    int8mm_block_set_test_skip, int8mm_block_set_wait_limit, int8mm_block_weight_bytes, int8mm_block_weight_codes)

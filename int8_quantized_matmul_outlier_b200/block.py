@@ -302,6 +302,16 @@ def int8mm_block_set_wait_limit(w: BlockWeight, timeout_ns: int) -> None:
     _check(lib().int8mm_block_set_wait_limit(w.handle, int(timeout_ns)))
 
 
+INT8MM_BLOCK_TEST_SKIP_SCALES = 1
+INT8MM_BLOCK_TEST_SKIP_MEETING = 2
+
+
+def int8mm_block_set_test_skip(w: BlockWeight, bits: int) -> None:
+    """Failure-detection tests only: later products leave out the arrivals
+    named by `bits` (INT8MM_BLOCK_TEST_SKIP_*), so a device wait runs out."""
+    _check(lib().int8mm_block_set_test_skip(w.handle, int(bits)))
+
+
 def int8mm_block_weight_bytes(w: BlockWeight) -> int:
     n = ctypes.c_size_t()
     _check(lib().int8mm_block_weight_bytes(w.handle, ctypes.byref(n)))

@@ -71,6 +71,8 @@ struct BlockGemmArgs {
   int tiles, last_rows;  // few rows: the RowsPlan's
   int* status;           // device status word
   unsigned long long timeout_ns;
+  int skip_scales;       // failure-detection tests only: one summing warp does not hand back its boxes of scales
+  int skip_meeting;      // likewise, few rows: CTA 0 of a cluster does not count itself at the others' meeting
 };
 
 // Largest K of this path, as of the rest of the library.

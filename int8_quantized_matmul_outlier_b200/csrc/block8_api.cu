@@ -31,6 +31,7 @@ struct int8mm_block_weight {
   int max_clusters[4] = {};  // of 1, 2, 4 and 8 CTAs, for products of few rows
   int* status = nullptr;
   unsigned long long timeout_ns = 2000000000ull;
+  int test_skip = 0;  // INT8MM_BLOCK_TEST_SKIP_* bits (failure-detection tests only)
   size_t bytes = 0;
 };
 
@@ -409,6 +410,8 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t handle, const void* code
   a.bf16 = dtype == INT8MM_DTYPE_BF16;
   a.status = h->status;
   a.timeout_ns = h->timeout_ns;
+  a.skip_scales = (h->test_skip & INT8MM_BLOCK_TEST_SKIP_SCALES) != 0;
+  a.skip_meeting = (h->test_skip & INT8MM_BLOCK_TEST_SKIP_MEETING) != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool few = M <= kRowsMaxM;
   const int width = few ? 0 : block_pair_width(M, N, K, h->num_sms);
@@ -495,6 +498,15 @@ int8mm_status int8mm_block_set_wait_limit(int8mm_block_weight_t handle, uint64_t
     return fail(INT8MM_ERR_INVALID_ARG, "timeout %llu ns is below the 1 ms minimum",
                 static_cast<unsigned long long>(timeout_ns));
   h->timeout_ns = timeout_ns;
+  return INT8MM_OK;
+}
+
+int8mm_status int8mm_block_set_test_skip(int8mm_block_weight_t handle, int bits) {
+  int8mm_block_weight* h = find(handle);
+  if (h == nullptr) return fail(INT8MM_ERR_INVALID_ARG, "invalid or freed weight handle");
+  if ((bits & ~(INT8MM_BLOCK_TEST_SKIP_SCALES | INT8MM_BLOCK_TEST_SKIP_MEETING)) != 0)
+    return fail(INT8MM_ERR_INVALID_ARG, "unknown test bits 0x%x", bits);
+  h->test_skip = bits;
   return INT8MM_OK;
 }
 

@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[chunk & 1u]);
+        if (lane == 0 && !(a.skip_scales && warp == 4 && rank == 0)) mbar_arrive(&sempty[chunk & 1u]);
       }
       const float bias = (n_ok && a.bias != nullptr) ? static_cast<float>(static_cast<const TY*>(a.bias)[n]) : 0.0f;
       TY* y = static_cast<TY*>(a.Y) + n;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
             // also where no token is theirs: a CTA that waited for nobody could
             // finish a tile before this one has noticed the end of the last,
             // and rempty would pass two phases unseen
-            mbar_arrive_cluster(bar);
+            if (!(a.skip_meeting && rank == 0)) mbar_arrive_cluster(bar);
           }
         }
         if (alive) alive = __all_sync(0xffffffffu, mbar_wait_cluster(rfull, tile & 1u, tmo, abort_flag));

@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[chunk & 1u]);
+        if (lane == 0 && !(a.skip_scales && warp == 4 && rank == 1)) mbar_arrive(&sempty[chunk & 1u]);
       }
       if (!alive) {
         if (lane == 0) gfail(a, abort_flag);
