@@ -341,7 +341,8 @@ void int8mm_free(int8mm_weight_t h);
  * to even, the quotients and the product in fp32; a = 0 gives scale 0 and
  * codes 0.  A group that holds Inf or NaN gets a scale of Inf or NaN and a
  * NaN code, so every output of a product that reads it is NaN.  A sum past
- * fp16's range becomes Inf.
+ * fp16's range becomes Inf.  The factor sx sw of a group is one fp32 product:
+ * scales whose product leaves fp32's range lose digits or become Inf.
  *
  * Layouts: activation codes [M, K] row-major; activation scales group-major,
  * sx[g][m] at scales[g * lds + m], g < ceil(K/128), with lds a multiple of 4
@@ -355,7 +356,9 @@ void int8mm_free(int8mm_weight_t h);
  * is not prepared on a stream that is being captured (INT8MM_ERR_INVALID_ARG),
  * and lives as long as the graphs that captured its products.  Besides
  * the weight a call uses only the caller's buffers: calls on several streams,
- * threads or captured graphs may share a handle.  Outputs may not
+ * threads or captured graphs may share a handle.  Calls with a handle run on
+ * its device; int8mm_block_quantize, int8mm_block_rms_norm and the two prepare
+ * calls run on the current device, to which stream and pointers belong.  Outputs may not
  * overlap inputs or each other unless the comment says so.  No call
  * allocates except the two prepare calls; none synchronises except
  * int8mm_block_get_status and int8mm_block_free.
@@ -396,7 +399,10 @@ int8mm_status int8mm_block_quantize(const void* X_dev, int dtype, int64_t M, int
  * itself (same pointer, row stride K).  normed [M, K] and codes + scales:
  * each may be NULL, not both; normed feeds layers that take 16-bit
  * activations, such as int8mm_forward.  The codes come from y in fp32, not
- * from its 16-bit rounding.  eps must be finite and >= 0.
+ * from its 16-bit rounding.  eps must be finite and >= 0.  The sum of squares
+ * is fp32: a bf16 row whose squares add up past its range (|h| from some 2^60
+ * on) comes out as 0, and with eps 0 a row whose squares vanish (|h| below
+ * 2^-75) as Inf, a row of zeros as NaN.
  */
 int8mm_status int8mm_block_rms_norm(const void* X_dev, int64_t ldx, const void* residual_dev, int64_t ldr,
                                     const void* weight_dev, int dtype, int64_t M, int64_t K, float eps,

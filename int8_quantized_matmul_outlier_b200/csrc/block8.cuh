@@ -60,10 +60,7 @@ cudaError_t launch_block_weight_unpack(const uint8_t* Wb, int64_t K, int64_t N, 
 struct BlockGemmArgs {
   int M, N, K;
   int N_pad;             // rows per group in the weight layout
-  const uint8_t* X;      // [M, K] codes
-  const uint8_t* Wb;
-  const float* sx;       // [G][lds]
-  int64_t lds;
+  const uint8_t* Wb;     // the codes of X and the scales sx come through tensor maps alone
   const float* sw;       // [N / 128][G]
   const void* bias;      // [N] of Y's type, or nullptr
   void* Y;               // [M, N]
@@ -80,10 +77,13 @@ constexpr int64_t kBlockMaxK = 65536;
 
 #ifdef __CUDACC__
 // Launch attribute that lets a kernel's blocks start while the stream's
-// previous kernel finishes; returns 1, the number of attributes written.  Each
-// kernel of this path calls dependency_wait() in every thread before it
-// touches global memory: what ran before it is then complete, and only its
-// setup overlaps.
+// previous kernel finishes; returns 1, the number of attributes written.  The
+// quantiser, the norm and the products are launched with it.  Every thread of
+// theirs calls dependency_wait() before it reads or writes global memory: what
+// ran before is then complete.  Ahead of it stands setup, and in the products a
+// prefetch of weight tiles into L2, which returns no data and needs no order
+// with their writer.  The kernels that prepare or read back a weight are
+// launched without the attribute and without the wait.
 inline unsigned overlap_attribute(cudaLaunchAttribute* attr) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr->val.programmaticStreamSerializationAllowed = 1;

@@ -46,9 +46,10 @@ __device__ __forceinline__ uint32_t max16(uint32_t m) {
 // ------------------------------------------------------------- quantiser
 // 16 lanes per group, 8 values per lane.  A warp takes a run of VPT * 4 groups
 // of a row, all its loads before the first use: the bytes in flight per SM,
-// not the arithmetic, set the rate.  Loads marked streaming, six blocks per
-// SM.  2048 x 20480 bf16 among others: 4 vectors per lane 23.8 us, 2 26.8;
-// with six blocks per SM 23.2, streaming 22.0 (5.7 TB/s).
+// not the arithmetic, set the rate.  Loads marked streaming, six blocks per SM
+// (40 registers, 8 bytes of spills).  2048 x 20480 bf16, back to back over four
+// inputs in turn: 4 vectors per lane 23.8 us, 2 26.8; with six blocks per SM
+// 23.2, streaming 22.0 (5.7 TB/s).  Over three inputs in turn it takes 25 us.
 constexpr int Q_THREADS = 256;
 
 template <typename T, int VPT>
@@ -87,10 +88,11 @@ __global__ void __launch_bounds__(Q_THREADS, 6) block_quantize_kernel(const Bloc
 // then residual_out = h, normed = round16(y), codes and scales of y (from
 // fp32, not from its 16-bit rounding).  h is rounded before the norm because
 // it is what the residual stream holds: the norm of residual_out alone gives
-// the same y.  Bound by memory: 2048 x 12288 fp16 with a residual takes 31.7
-// us among others, 5.6 TB/s of its 7 bytes per value (33.1 with plain stores of
-// residual_out; 512 threads per row 32.7, 128 threads 40).  TPR threads hold a row in registers, VPT vectors of 8 values
-// each; the sum of squares is fp32, in a fixed order.
+// the same y.  Bound by memory: 2048 x 12288 fp16 with a residual, back to back
+// over four inputs in turn, takes 32 us, 5.5 TB/s of its 7 bytes per value (33.1
+// with plain stores of residual_out; 512 threads per row 32.7, 128 threads 40);
+// over three inputs in turn 35 us.  TPR threads hold a row in registers, VPT
+// vectors of 8 values each; the sum of squares is fp32, in a fixed order.
 template <typename T, int TPR, int VPT, int THREADS>
 __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowArgs a) {
   constexpr int ROWS = THREADS / TPR, WPR = TPR / 32;
@@ -129,7 +131,8 @@ __global__ void __launch_bounds__(THREADS) block_rms_norm_kernel(const BlockRowA
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], r[i]);
           h[j0 + j] = pack8<T>(x);
-          __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.K) + c, h[j0 + j]);  // read much later
+          // streaming: read much later
+          __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.K) + c, h[j0 + j]);
         }
       }
     }
@@ -186,7 +189,10 @@ cudaError_t norm_t(const BlockRowArgs& a, cudaStream_t stream) {
 // Threads per row and vectors per thread.  Few rows: as many threads as the
 // row has vectors, up to 1024, for the shortest chain.  Many rows: 256 threads
 // with up to 8 vectors each, so that several rows per SM are under way and
-// one's loads run under another's sums and stores.
+// one's loads run under another's sums and stores.  That ends at K = 16384:
+// longer rows take 1024 threads and one or two rows are under way per SM (2048
+// rows with a residual: K = 16384 50.6 us, 4.6 TB/s; 20480 71.9, 4.1; 32768
+// 99.5, 4.7).  <1024, 8>, from K = 32784 on, spills 84 bytes.
 template <typename T>
 cudaError_t norm_d(const BlockRowArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t nvec = a.K / 8;

@@ -400,10 +400,7 @@ int8mm_status int8mm_block_matmul(int8mm_block_weight_t handle, const void* code
   a.N = static_cast<int>(N);
   a.K = static_cast<int>(K);
   a.N_pad = static_cast<int>(h->N_pad);
-  a.X = static_cast<const uint8_t*>(codes_dev);
   a.Wb = h->Wb;
-  a.sx = scales_dev;
-  a.lds = lds;
   a.sw = h->sw;
   a.bias = bias_dev;
   a.Y = Y_dev;

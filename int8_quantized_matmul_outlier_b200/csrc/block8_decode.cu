@@ -14,9 +14,10 @@
 // cluster: CTA r finishes the tokens [r MP / S, (r + 1) MP / S), adding the S
 // parts in the order of the ranks; the parts travel as one bulk copy per pair
 // of CTAs (stored value by value from the registers into the peers' memory,
-// 32 tokens at K = N = 8192 took 36.9 us, 14 more than one token).  No workspace, no atomics, and the same
-// result every time.  Splitting N alone would leave SMs idle at small N and
-// the last round part-filled; splitting K alone would need the sum in memory.
+// 32 tokens at K = N = 8192 took 36.9 us, 14 more than one token).  No
+// workspace, no atomics, and the same result every time.  Splitting N alone
+// would leave SMs idle at small N and the last round part-filled; splitting K
+// alone would need the sum in memory.
 //   warp 0      TMA producer (W marked evict-first in L2), GS groups per stage
 //   warp 1      TMEM, MMA issuer
 //   warps 4..   sums: one row n per thread; with 64 or more tokens two warps
@@ -24,6 +25,11 @@
 // Two groups per stage: a step's waits take each of these
 // warps some 500 cycles, a group's 16 KB of W some 700 at the SM's share of
 // the HBM rate.
+//
+// Measured in a captured chain, weights in turn: 1 x 12288 x 49152 95.0 us, 97%
+// of the measured copy rate (one weight again and again 92.4, of which a part
+// is still in L2; back to back over three weights 92 to 98 on several
+// machines), 32 x 8192 x 8192 16.8 us, of which the stream of W is 10.4.
 //
 // Every wait is bounded; a timeout sets the status word, and the CTA drains
 // and exits with its cluster.
@@ -95,8 +101,8 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
 // Copy of `bytes` (a multiple of 16) from this CTA's shared memory to a
 // cluster address, counted on the barrier there.
 __device__ __forceinline__ void bulk_to_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "r"(src), "r"(bytes), "r"(bar)
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "r"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
 __device__ __forceinline__ void epi_sync(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
@@ -152,8 +158,8 @@ __device__ __forceinline__ void rows_wait(uint32_t (&r)[N]) {
 
 // tmW: the weight's rows of 128 bytes with 128-row boxes; tmWl with boxes of
 // a.last_rows, the rows of the longest run's last tile (a shorter run's last
-// tile reads 16 rows too many, and drops them); tmX: the codes [M, K] with MP-row boxes; tmS: the scales [G][M] with
-// 16 x MP boxes.
+// tile reads 16 rows too many, and drops them); tmX: the codes [M, K] with
+// MP-row boxes; tmS: the scales [G][M] with 16 x MP boxes.
 template <int MP, typename TY>
 __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
     block_gemm_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWl,
@@ -217,8 +223,9 @@ __global__ void __launch_bounds__(RCfg<MP>::THREADS, 1)
   const unsigned long long tmo = a.timeout_ns;
   if (warp == 0 && relect_one()) {
     // The first tiles of W into L2 while the stream's previous kernel ends: a
-    // hint that needs no order with it.  16 x 8192 x 8192 among others 16.7 ->
-    // 15.2 us, 1 x 12288 x 49152 94.8 -> 91.7.
+    // hint that needs no order with it.  In a captured chain 16 x 8192 x 8192
+    // (four weights in turn) 16.7 -> 15.2 us, 1 x 12288 x 49152 (one weight)
+    // 94.8 -> 92.
     const uint32_t bytes = static_cast<uint32_t>(min(RM, row_end - row_begin) * kGroup);
     for (int g = g_begin; g < min(g_end, g_begin + C::STAGES * C::GS); ++g)
       bulk_prefetch_l2(a.Wb + (static_cast<size_t>(g) * a.N_pad + row_begin) * kGroup, bytes);
@@ -513,8 +520,12 @@ cudaError_t rows_max_clusters(int S, int* clusters) {
 // fullest CTA, in rows x groups (2.8 ns each at an SM's share of the HBM
 // rate).  A tile of fewer than 48 rows takes the time of 48.  The meeting of a
 // tile's sums takes MEET, and where another tile follows, whose MMAs then wait
-// for it, MEET_M per token more: N = K = 8192 takes 24.6 us unsplit and 23.6
-// in pairs with 32 tokens, K = 12288, N = 49152 (six tiles) 100 and 127.
+// for it, MEET_M per token more.  The constants were fitted before the first
+// tiles were prefetched; the choice still holds where splits of 1, 2 and 4 were
+// timed after it (captured, us): N = K = 8192 16 tokens 16.2, 13.7, 20.3, 32
+// tokens 19.6, 16.3, 21.7, 64 tokens 22.1, 18.0, 23.7; K = 5120, N = 20480, 32
+// tokens 27.2, 34.2, 42.9; K = 12288, N = 49152 (unsplit three tiles) 1 token
+// 92.5, 105, 127, 32 tokens 93.1, 118, 145.
 RowsPlan rows_plan(int64_t M, int64_t N, int64_t K, const int (&max_clusters)[4]) {
   constexpr int64_t MEET = 700, MEET_M = 40, UNSPLIT = 200;
   const int64_t units = N / 16, G = block_groups(K);

@@ -30,14 +30,23 @@
 // warp polls its barriers together or ahead of need, and the scales come in
 // boxes of 16 groups.
 //
-// What bounds it: the sums.  Adding 128 x 256 values takes the eight warps 262
-// cycles, and their reads, polls and arrivals as much again.  Time over groups,
-// tile ends included, is 480 to 520 ns at 256 columns and 235 to 255 at 128 for
-// K of 8192 and more (2048 x 12288 x 49152: 1030 us either way, 0.74 of twice
-// the measured bf16 rate; 2048 x 8192 x 8192: 133 and 115 us); with the
-// multiply-adds left out 200 to 227 at 128.  The tensor cores' own time is 260
-// and 130.  Under load the power cap takes the
-// clock to 1.43 GHz, and 2048 x 12288 x 49152 to 1220 us.
+// What bounds it: no unit alone.  Time over groups of the fullest pair, tile
+// ends included, at 2048 x 12288 x 49152, and with parts left out in scratch
+// builds (ns; alone, at 128 and 256 columns):
+//   all                                261   518
+//   without the multiply-adds          221   422
+//   nor the reads of the sums          218   404
+//   nor the MMAs: loads and barriers   179   252
+// The tensor cores' own time is 130 and 260, the multiply-adds' (128 x 128 and
+// 128 x 256 by eight warps) 67 and 133.  At 128 columns the loads, 24 KB per SM
+// and group from L2 (20 TB/s over all SMs), are most of it, and MMAs and loads
+// together, which meet in shared memory, nearly all the rest; at 256 columns
+// the loads are lighter per column, and the chain of a group (MMAs, poll, read,
+// hand-back, adds) is what does not overlap.  Per column the two are equal.
+// 2048 x 12288 x 49152 takes 1030 to 1073 us alone over several machines, 0.71
+// to 0.74 of twice the measured bf16 rate; 2048 x 8192 x 8192 115 us at 128
+// columns and 132 at 256.  Back to back the power cap takes the clock to 1.43
+// GHz, and 2048 x 12288 x 49152 to 1230 to 1265 us.
 //
 // BN: 256 or 128, by the pairs' rounds (block_pair_width).  Widths of 160 and
 // 192, whose halves straddle blocks of the weight scales, took 5% and 18% more

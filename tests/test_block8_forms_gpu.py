@@ -94,3 +94,17 @@ def test_product_over_several_tiles_and_boxes_of_scales(M, K, N, dtype):
         assert torch.equal(m.int8mm_block_matmul(w, codes, scales, bias=bias, dtype=dtype), y)
     assert torch.equal(m.int8mm_block_forward(w, x, bias=bias), y)
     assert m.int8mm_block_get_status(w) == m.INT8MM_OK
+
+
+@pytest.mark.parametrize("K", [256, 1040, 12288])
+def test_norm_where_the_squares_leave_fp32(K):
+    """As the header says: 0 past the range, Inf (NaN for 0) below it without an eps; other rows are not touched."""
+    x = acts(6, K, BF16, 1)
+    want = m.int8mm_block_rms_norm(x, torch.ones(K, dtype=BF16, device=dev()), 0.0, normed=True)
+    x[1], x[3], x[4] = 2.0 ** 70, 2.0 ** -80, 0.0
+    codes, scales, _, y = m.int8mm_block_rms_norm(x, torch.ones(K, dtype=BF16, device=dev()), 0.0, normed=True)
+    assert (y[1] == 0).all() and (codes[1].float() == 0).all() and (scales[1] == 0).all()
+    assert (y[3] == float("inf")).all() and y[4].isnan().all() and scales[4].isnan().all()
+    keep = [0, 2, 5]
+    assert torch.equal(y[keep], want[3][keep]) and torch.equal(scales[keep], want[1][keep])
+    assert torch.equal(bits(codes[keep]), bits(want[0][keep]))
