@@ -353,12 +353,13 @@ void int8mm_free(int8mm_weight_t h);
  * are below 2^31.  Pointers are 16-byte aligned.
  *
  * A handle may be used on any stream ordered after its preparation.  A weight
- * is not prepared on a stream that is being captured (INT8MM_ERR_INVALID_ARG),
- * and lives as long as the graphs that captured its products.  Besides
- * the weight a call uses only the caller's buffers: calls on several streams,
- * threads or captured graphs may share a handle.  Calls with a handle run on
- * its device; int8mm_block_quantize, int8mm_block_rms_norm and the two prepare
- * calls run on the current device, to which stream and pointers belong.  Outputs may not
+ * cannot be prepared on a stream that is being captured
+ * (INT8MM_ERR_INVALID_ARG), and must outlive the graphs that captured its
+ * products.  Besides the weight a call uses only the caller's buffers: calls
+ * on several streams, threads or captured graphs may share a handle.  Calls
+ * with a handle run on its device; int8mm_block_quantize,
+ * int8mm_block_rms_norm and the two prepare calls run on the current device,
+ * to which stream and pointers belong.  Outputs may not
  * overlap inputs or each other unless the comment says so.  No call
  * allocates except the two prepare calls; none synchronises except
  * int8mm_block_get_status and int8mm_block_free.

@@ -329,9 +329,9 @@ class LinearBlock8bit(torch.nn.Module):
 
     x is fp16 or bf16 [..., in_features], or a pair (codes, scales) as
     ``RMSNormBlock8bit`` and ``int8mm_block_quantize`` give it (the output is
-    then [M, out_features] of ``dtype``).  The 16-bit weight is not kept.  The state dict holds
-    the weight as ``weight_codes`` and ``weight_scales``; loading one prepares
-    a new weight."""
+    then [M, out_features] of ``dtype``).  The 16-bit weight is not kept.  The
+    state dict holds the weight as ``weight_codes`` and ``weight_scales``;
+    loading one prepares a new weight."""
 
     def __init__(self, weight: BlockWeight, bias: torch.Tensor | None = None, dtype: torch.dtype = torch.float16):
         super().__init__()
